@@ -12,6 +12,9 @@ Entry points (same names as the C functions):
   diffattn_fwd_decode           V2 split-KV decode (and diffattn_fwd_decode_static)
   diffattn_fwd_decode_v1        V1 split-KV decode with the per-head norm
   diffattn_fwd_decode_paged     either decode over a paged cache (block table)
+  diffattn_kv4_write            K and V rows into a KV cache held in 4 bits (contiguous, paged)
+  diffattn_kv4_read             its values, back in rows
+  diffattn_fwd_decode_kv4       the V2 and V1 decode over such a cache
   diffattn_bwd_prefill          gradients dq, dk, dv, dlambda of the prefill
   diffattn_lambda_bwd           gradients of the four lambda vectors
 """
@@ -29,6 +32,11 @@ from ._binding import (  # noqa: F401
     diffattn_fwd_decode_static,
     diffattn_fwd_decode_v1,
     diffattn_fwd_decode_paged,
+    diffattn_kv4_write,
+    diffattn_kv4_read,
+    diffattn_fwd_decode_kv4,
+    diffattn_decode_kv4_workspace_size,
+    KV4_RECORD_BYTES,
     diffattn_selftest_timeout,
     diffattn_selftest_exp2,
     diffattn_debug_bounds_violations,
@@ -52,6 +60,11 @@ __all__ = [
     "diffattn_fwd_decode_static",
     "diffattn_fwd_decode_v1",
     "diffattn_fwd_decode_paged",
+    "diffattn_kv4_write",
+    "diffattn_kv4_read",
+    "diffattn_fwd_decode_kv4",
+    "diffattn_decode_kv4_workspace_size",
+    "KV4_RECORD_BYTES",
     "diffattn_selftest_timeout",
     "diffattn_selftest_exp2",
     "diffattn_debug_bounds_violations",

@@ -43,6 +43,10 @@ EXPORTS = (
     "diffattn_fwd_decode_static",
     "diffattn_fwd_decode_v1",
     "diffattn_fwd_decode_paged",
+    "diffattn_kv4_write",
+    "diffattn_kv4_read",
+    "diffattn_decode_kv4_workspace_size",
+    "diffattn_fwd_decode_kv4",
     "diffattn_selftest_timeout",
     "diffattn_selftest_exp2",
     "diffattn_debug_bounds_violations",
@@ -89,6 +93,20 @@ class DecodeParams(ctypes.Structure):
         ("q_strides", ctypes.c_int64 * 2),
         ("kv_strides", ctypes.c_int64 * 3),
         ("o_strides", ctypes.c_int64 * 2),
+    ]
+
+
+class Kv4Rows(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32),
+        ("batch", ctypes.c_int32),
+        ("n_tokens", ctypes.c_int32),
+        ("max_seqlen", ctypes.c_int32),
+        ("n_kv_heads", ctypes.c_int32),
+        ("max_kv_len", ctypes.c_int32),
+        ("k_strides", ctypes.c_int64 * 3),
+        ("v_strides", ctypes.c_int64 * 3),
+        ("cache_strides", ctypes.c_int64 * 3),
     ]
 
 
@@ -159,6 +177,16 @@ def load_library():
     lib.diffattn_selftest_exp2.argtypes = [vp, vp, vp, i32, vp]
     lib.diffattn_debug_bounds_violations.restype = i32
     lib.diffattn_debug_bounds_violations.argtypes = [ctypes.POINTER(ctypes.c_int32)]
+    lib.diffattn_kv4_write.restype = i32
+    lib.diffattn_kv4_write.argtypes = [ctypes.POINTER(Kv4Rows), vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.diffattn_kv4_read.restype = i32
+    lib.diffattn_kv4_read.argtypes = [ctypes.POINTER(Kv4Rows), vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.diffattn_decode_kv4_workspace_size.restype = i32
+    lib.diffattn_decode_kv4_workspace_size.argtypes = [ctypes.POINTER(DecodeParams),
+                                                       ctypes.POINTER(ctypes.c_size_t)]
+    lib.diffattn_fwd_decode_kv4.restype = i32
+    lib.diffattn_fwd_decode_kv4.argtypes = [ctypes.POINTER(DecodeParams), vp, vp, vp, vp, vp, f32p, f32p,
+                                            i32, ctypes.c_float, vp, vp, ctypes.c_size_t, vp, vp]
     _lib = lib
     return lib
 
@@ -568,6 +596,228 @@ def diffattn_fwd_decode_static(q, k_cache, v_cache, lam, kv_len=None, out=None, 
                                         _ptr(kv_len), _ptr(lam), _ptr(out), _ptr(dev_status),
                                         _stream(stream))
     _check("diffattn_fwd_decode_static", rc)
+    return out
+
+
+KV4_RECORD_BYTES = 144  # DIFFATTN_KV4_RECORD_BYTES
+
+
+def _kv4_fail(fn, why, status=-1):
+    e = DiffattnError(fn, status)
+    e.args = (f"{e.args[0]}: {why}",)
+    raise e
+
+
+def _kv4_tensor(fn, name, t, dtype, device, shape=None, dense=True):
+    """Refuse an operand of another dtype, device, shape or (where the library takes no
+    strides for it) a strided one."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        _kv4_fail(fn, f"{name} is {t.dtype}, not {dtype}", -2)
+    if t.device != device:
+        _kv4_fail(fn, f"{name} is on {t.device}, the cache on {device}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        _kv4_fail(fn, f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if dense and not t.is_contiguous():
+        _kv4_fail(fn, f"{name} must be contiguous")
+
+
+def _kv4_cache(fn, cache, block_table, max_kv_len, batch):
+    """(pool geometry or None, byte strides, positions of an entry) of a cache tensor."""
+    import torch
+    if cache.dtype != torch.uint8:
+        _kv4_fail(fn, f"cache is {cache.dtype}, not torch.uint8", -2)
+    if not cache.is_cuda:
+        _kv4_fail(fn, "cache is not a CUDA tensor")
+    if cache.dim() != 4 or cache.shape[3] != KV4_RECORD_BYTES or cache.stride(3) != 1:
+        _kv4_fail(fn, f"cache must be [entries or pages, tokens, heads, {KV4_RECORD_BYTES}] with whole records")
+    if block_table is None:
+        if cache.shape[0] != batch:
+            _kv4_fail(fn, f"cache holds {cache.shape[0]} entries, the batch {batch}")
+        room = int(cache.shape[1])
+        L = room if max_kv_len is None else int(max_kv_len)
+        if L > room:
+            _kv4_fail(fn, f"max_kv_len {L} is past the cache's {room} positions")
+        return None, cache.stride()[:3], L
+    if block_table.dim() != 2 or block_table.shape[0] != batch:
+        _kv4_fail(fn, f"block_table has shape {tuple(block_table.shape)}, the batch is {batch}")
+    _kv4_tensor(fn, "block_table", block_table, torch.int32, cache.device)
+    pk = PagedKV()
+    pk.num_pages, pk.page_size = int(cache.shape[0]), int(cache.shape[1])
+    pk.max_pages_per_seq = int(block_table.shape[1])
+    pk.page_strides[:] = cache.stride()[:3]
+    L = pk.page_size * pk.max_pages_per_seq if max_kv_len is None else int(max_kv_len)
+    return pk, (0, 0, 0), L
+
+
+def _kv4_scope(device, stream):
+    """Make the cache's device and the launch stream current, so that allocations belong to
+    that stream and a call on tensors of another device than the current one lands there."""
+    import contextlib
+
+    import torch
+    scope = contextlib.ExitStack()
+    if torch.cuda.current_device() != device.index:
+        scope.enter_context(torch.cuda.device(device))
+    if stream is not None:
+        if stream.device != device:
+            _kv4_fail("stream", f"the stream is on {stream.device}, the cache on {device}")
+        scope.enter_context(torch.cuda.stream(stream))
+    return scope
+
+
+def _kv4_rows(fn, k, v, cache, pos, cu_seqlens, max_seqlen, block_table, max_kv_len, dev_status):
+    """Parameter struct and pool geometry of a write or a read of rows k and v."""
+    import torch
+    packed = cu_seqlens is not None
+    lead = 1 if packed else 2
+    for name, t in (("k", k), ("v", v)):
+        _kv4_tensor(fn, name, t, k.dtype, cache.device, dense=False)
+        if t.dim() not in (lead + 2, lead + 3) or t.shape[lead + 1:].numel() != 128:
+            _kv4_fail(fn, f"{name} has shape {tuple(t.shape)}: rows of 128 channels behind "
+                          + ("[rows, heads]" if packed else "[batch, rows, heads]"))
+        if t.stride(-1) != 1 or (t.dim() == lead + 3 and t.stride(-2) != t.shape[-1]):
+            _kv4_fail(fn, f"the 128 channels of {name} must be contiguous")
+        if t.shape[:lead + 1] != k.shape[:lead + 1]:
+            _kv4_fail(fn, f"k and v differ in rows or heads: {tuple(k.shape)}, {tuple(v.shape)}")
+    if cache.dim() == 4 and k.shape[lead] != cache.shape[2]:
+        _kv4_fail(fn, f"k has {k.shape[lead]} heads, the cache {cache.shape[2]}")
+    if packed:
+        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+            _kv4_fail(fn, "cu_seqlens must be [batch + 1]")
+        _kv4_tensor(fn, "cu_seqlens", cu_seqlens, torch.int32, cache.device)
+        if max_seqlen is None:
+            _kv4_fail(fn, "cu_seqlens needs max_seqlen, the most rows of an entry")
+    p = Kv4Rows()
+    p.dtype = _dtype_code(k)
+    p.batch = int(cu_seqlens.shape[0]) - 1 if packed else int(k.shape[0])
+    p.n_tokens = int(k.shape[lead - 1])
+    p.max_seqlen = int(max_seqlen) if packed else 0
+    p.n_kv_heads = int(k.shape[lead])
+    p.k_strides[:] = (0, *k.stride()[:2]) if packed else k.stride()[:3]
+    p.v_strides[:] = (0, *v.stride()[:2]) if packed else v.stride()[:3]
+    pk, p.cache_strides[:], p.max_kv_len = _kv4_cache(fn, cache, block_table, max_kv_len, p.batch)
+    _kv4_tensor(fn, "pos", pos, torch.int32, cache.device, (p.batch,))
+    _kv4_tensor(fn, "dev_status", dev_status, torch.int32, cache.device)
+    return p, None if pk is None else ctypes.byref(pk)
+
+
+def diffattn_kv4_write(k, v, cache, pos=None, cu_seqlens=None, max_seqlen=None, block_table=None,
+                       max_kv_len=None, dev_status=None, stream=None):
+    """Quantise rows of K and V into a 4-bit cache (see include/diffattn.h): row i of entry b
+    becomes the record at position pos[b] + i (pos int32 [B], None = 0). k, v bf16 or float32
+    [B,N,H,128] (V1's k [B,N,H,2,64] alike), or packed [rows,H,128] with cu_seqlens int32
+    [B+1] and max_seqlen. cache uint8 [B,L,H,144], or a pool [P,page,H,144] with block_table.
+    Returns cache."""
+    lib = load_library()
+    p, pk = _kv4_rows("diffattn_kv4_write", k, v, cache, pos, cu_seqlens, max_seqlen, block_table,
+                      max_kv_len, dev_status)
+    with _kv4_scope(cache.device, stream):
+        rc = lib.diffattn_kv4_write(ctypes.byref(p), pk, _ptr(k), _ptr(v), _ptr(cu_seqlens), _ptr(pos),
+                                    _ptr(cache), _ptr(block_table), _ptr(dev_status), _stream(stream))
+    _check("diffattn_kv4_write", rc)
+    return cache
+
+
+def diffattn_kv4_read(cache, n_tokens=None, pos=None, cu_seqlens=None, max_seqlen=None,
+                      block_table=None, max_kv_len=None, k=None, v=None, dtype=None,
+                      dev_status=None, stream=None):
+    """Rows of K and V back from a 4-bit cache (see include/diffattn.h): n_tokens rows of each
+    entry from position pos[b] on, or with cu_seqlens n_tokens packed rows in all. Returns
+    (k, v), new tensors [B,N,H,128] or [rows,H,128] of `dtype` (default bf16) unless given;
+    V1's k is the same rows viewed as [..., H, 2, 64]."""
+    import torch
+    lib = load_library()
+    if (k is None) != (v is None):
+        _kv4_fail("diffattn_kv4_read", "give both k and v or neither")
+    with _kv4_scope(cache.device, stream):
+        if k is None:
+            if n_tokens is None or cache.dim() != 4:
+                _kv4_fail("diffattn_kv4_read", "needs n_tokens or k and v, and a cache [., ., H, 144]")
+            rows = (int(n_tokens),)
+            if cu_seqlens is None:
+                rows = (int(cache.shape[0] if block_table is None else block_table.shape[0]), *rows)
+            k = torch.empty((*rows, cache.shape[2], 128), dtype=dtype or torch.bfloat16, device=cache.device)
+            v = torch.empty_like(k)
+        elif (n_tokens is not None and int(n_tokens) != k.shape[0 if cu_seqlens is not None else 1]) or (
+                dtype is not None and dtype != k.dtype):
+            _kv4_fail("diffattn_kv4_read", "n_tokens or dtype is not that of the given k")
+        p, pk = _kv4_rows("diffattn_kv4_read", k, v, cache, pos, cu_seqlens, max_seqlen, block_table,
+                          max_kv_len, dev_status)
+        rc = lib.diffattn_kv4_read(ctypes.byref(p), pk, _ptr(cache), _ptr(block_table), _ptr(cu_seqlens),
+                                   _ptr(pos), _ptr(k), _ptr(v), _ptr(dev_status), _stream(stream))
+    _check("diffattn_kv4_read", rc)
+    return k, v
+
+
+def decode_kv4_params(q, cache, out, num_splits=0, block_table=None, max_kv_len=None):
+    """(DecodeParams, pool geometry or None) of a decode over a 4-bit cache; `out` may be None
+    (its strides are then those of a dense output)."""
+    fn = "diffattn_fwd_decode_kv4"
+    v1 = q.dim() == 4
+    if q.dim() not in (3, 4) or (v1 and q.shape[2] != 2):
+        _kv4_fail(fn, f"q has shape {tuple(q.shape)}: V2 [B, Hq, 128], V1 [B, H, 2, 64]")
+    if q.stride(-1) != 1 or (v1 and q.stride(2) != q.shape[3]):
+        _kv4_fail(fn, "the channels of q must be contiguous")
+    p = DecodeParams()
+    p.variant = DIFFATTN_V1 if v1 else DIFFATTN_V2
+    p.dtype = _dtype_code(q)
+    p.batch, p.n_q_heads, p.head_dim = int(q.shape[0]), int(q.shape[1]), int(q.shape[-1])
+    p.num_splits = int(num_splits)
+    pk, p.kv_strides[:], p.max_kv_len = _kv4_cache(fn, cache, block_table, max_kv_len, p.batch)
+    p.n_kv_heads = int(cache.shape[2])
+    p.q_strides[:] = q.stride()[:2]
+    units = p.n_q_heads if v1 else p.n_q_heads // 2
+    p.o_strides[:] = (units * 128, 128) if out is None else out.stride()[:2]
+    return p, pk
+
+
+def diffattn_decode_kv4_workspace_size(p: DecodeParams) -> int:
+    n = ctypes.c_size_t(0)
+    _check("diffattn_decode_kv4_workspace_size",
+           load_library().diffattn_decode_kv4_workspace_size(ctypes.byref(p), ctypes.byref(n)))
+    return int(n.value)
+
+
+def diffattn_fwd_decode_kv4(q, cache, lam, kv_len=None, lambda_init=None, out=None, apply_norm=None,
+                            norm_eps=1e-5, workspace=None, num_splits=0, block_table=None,
+                            max_kv_len=None, dev_status=None, stream=None):
+    """Split-KV differential decode over a 4-bit cache (see include/diffattn.h): uint8
+    [B,L,H,144], or a pool [P,page,H,144] with block_table int32 [B,pages]. V2: q [B,Hq,128] ->
+    out [B,Hq/2,128]. V1: q [B,H,2,64] -> out [B,H,128] (norm and scale when apply_norm, default
+    on). max_kv_len defaults to the positions the cache or the block table has room for."""
+    import torch
+    fn = "diffattn_fwd_decode_kv4"
+    lib = load_library()
+    p, pk = decode_kv4_params(q, cache, out, num_splits, block_table, max_kv_len)
+    v1 = p.variant == DIFFATTN_V1
+    norm = v1 if apply_norm is None else bool(apply_norm)
+    units = p.n_q_heads if v1 else p.n_q_heads // 2
+    device = cache.device
+    _kv4_tensor(fn, "q", q, torch.bfloat16, device, dense=False)
+    _kv4_tensor(fn, "lam", lam, torch.float32, device, (units,))
+    _kv4_tensor(fn, "kv_len", kv_len, torch.int32, device, (p.batch,))
+    _kv4_tensor(fn, "lambda_init", lambda_init, torch.float32, device)
+    _kv4_tensor(fn, "dev_status", dev_status, torch.int32, device)
+    if out is not None:
+        _kv4_tensor(fn, "out", out, torch.bfloat16, device, (p.batch, units, 128), dense=False)
+        if out.stride(-1) != 1:
+            _kv4_fail(fn, "the channels of out must be contiguous")
+    need = diffattn_decode_kv4_workspace_size(p)
+    with _kv4_scope(device, stream):
+        if out is None:
+            out = torch.empty((p.batch, units, 128), dtype=torch.bfloat16, device=device)
+        if workspace is None and need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        if workspace is not None and (workspace.device != device or not workspace.is_contiguous()):
+            _kv4_fail(fn, "workspace must be contiguous and on the cache's device", -4)
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        rc = lib.diffattn_fwd_decode_kv4(
+            ctypes.byref(p), None if pk is None else ctypes.byref(pk), _ptr(q), _ptr(cache), _ptr(block_table),
+            _ptr(kv_len), _ptr(lam), _ptr(lambda_init), int(norm), float(norm_eps), _ptr(out), _ptr(workspace),
+            ws_bytes, _ptr(dev_status), _stream(stream))
+    _check(fn, rc)
     return out
 
 

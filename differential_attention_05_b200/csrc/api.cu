@@ -585,3 +585,192 @@ int diffattn_fwd_decode_paged(const diffattn_decode_params* p, const diffattn_pa
 }
 
 }  // extern "C"
+
+// ---- a KV cache held in 4 bits ---------------------------------------------------------
+
+// The cache of the entry points below from its layout: byte strides of a contiguous cache, or
+// the pool geometry when pk is given. B, H, L are validated by the caller.
+static int kv4_cache_setup(const diffattn_paged_kv* pk, const int64_t* strides, int B, int H, int L,
+                           const void* cache, const int32_t* block_table, int* dev_status, Kv4Cache* c) {
+  memset(c, 0, sizeof(*c));
+  const int64_t* s = pk ? pk->page_strides : strides;
+  if (!strides_ok(s, 3)) return DIFFATTN_ERR_INVALID_ARG;
+  if (pk) {
+    if (pk->page_size < 1 || pk->page_size > 65536 || (pk->page_size & (pk->page_size - 1)))
+      return DIFFATTN_ERR_INVALID_ARG;
+    if (pk->num_pages < 1 || pk->max_pages_per_seq < 1 || pk->reserved != 0) return DIFFATTN_ERR_INVALID_ARG;
+    if ((int64_t)pk->max_pages_per_seq * pk->page_size < L) return DIFFATTN_ERR_INVALID_ARG;
+    while ((1 << c->page_shift) < pk->page_size) ++c->page_shift;
+    c->block_table = block_table;
+    c->bt_stride = pk->max_pages_per_seq;
+    c->num_pages = pk->num_pages;
+  }
+  if (s[0] % 16 || s[1] % 16 || s[2] % 16 || !aligned16(cache)) return DIFFATTN_ERR_MISALIGNED;
+  // records must not overlap along any axis that has more than one
+  const int64_t rec = DIFFATTN_KV4_RECORD_BYTES;
+  const int64_t outer = pk ? pk->num_pages : B, rows = pk ? pk->page_size : L;
+  if ((outer > 1 && s[0] < rec) || (rows > 1 && s[1] < rec) || (H > 1 && s[2] < rec))
+    return DIFFATTN_ERR_INVALID_ARG;
+  c->base = static_cast<uint8_t*>(const_cast<void*>(cache));
+  memcpy(c->stride, s, sizeof(c->stride));
+  c->L = L;
+  c->ext = extent(outer, rows, H, rec, s);
+  c->ext_bt = pk ? (int64_t)B * pk->max_pages_per_seq : 0;
+  c->dev_status = dev_status;
+  c->dbg_status = debug_status_word();
+  return DIFFATTN_OK;
+}
+
+static int kv4_rows_run(bool write, const diffattn_kv4_rows* p, const diffattn_paged_kv* pk, const void* k,
+                        const void* v, const int32_t* cu_seqlens, const int32_t* pos, const void* cache,
+                        const int32_t* block_table, int* dev_status, void* stream) {
+  if (!p) return DIFFATTN_ERR_INVALID_ARG;
+  if (p->dtype != DIFFATTN_F32 && p->dtype != DIFFATTN_BF16) return DIFFATTN_ERR_INVALID_ARG;
+  const int per = cu_seqlens ? p->max_seqlen : p->n_tokens;
+  if (p->batch < 0 || p->n_tokens < 0 || per < 0 || p->n_kv_heads < 1 || p->max_kv_len < 0)
+    return DIFFATTN_ERR_INVALID_ARG;
+  if (p->batch > 65535 || p->n_kv_heads > 65535 || p->max_kv_len > (1 << 30)) return DIFFATTN_ERR_UNSUPPORTED;
+  if ((int64_t)per * p->n_kv_heads > (int64_t)1 << 35) return DIFFATTN_ERR_UNSUPPORTED;  // the launch's grid
+  if (!strides_ok(p->k_strides, 3) || !strides_ok(p->v_strides, 3)) return DIFFATTN_ERR_INVALID_ARG;
+  Kv4RowsArgs a;
+  memset(&a, 0, sizeof(a));
+  const int rc = kv4_cache_setup(pk, p->cache_strides, p->batch, p->n_kv_heads, p->max_kv_len, cache,
+                                 block_table, dev_status, &a.cache);
+  if (rc != DIFFATTN_OK) return rc;
+  if (p->batch == 0 || p->n_tokens == 0 || per == 0) return DIFFATTN_OK;
+  if (!k || !v || !cache || (pk && !block_table)) return DIFFATTN_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v)) return DIFFATTN_ERR_MISALIGNED;
+  const int64_t unit = p->dtype == DIFFATTN_F32 ? 4 : 8;
+  for (int i = cu_seqlens ? 1 : 0; i < 3; ++i)
+    if (p->k_strides[i] % unit || p->v_strides[i] % unit) return DIFFATTN_ERR_MISALIGNED;
+  a.B = p->batch;
+  a.H = p->n_kv_heads;
+  a.N = per;
+  a.total = p->n_tokens;
+  a.f32 = p->dtype == DIFFATTN_F32;
+  a.cu = cu_seqlens;
+  a.pos = pos;
+  a.k = const_cast<void*>(k);
+  a.v = const_cast<void*>(v);
+  memcpy(a.ks, p->k_strides, sizeof(a.ks));
+  memcpy(a.vs, p->v_strides, sizeof(a.vs));
+  const int64_t nb = cu_seqlens ? 1 : a.B;
+  a.ext_k = extent(nb, p->n_tokens, a.H, 128, a.ks);
+  a.ext_v = extent(nb, p->n_tokens, a.H, 128, a.vs);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return from_cuda(write ? launch_kv4_write(a, s) : launch_kv4_read(a, s));
+}
+
+static int decode_kv4_check(const diffattn_decode_params* p, int* splits, int* split_len) {
+  if (!p) return DIFFATTN_ERR_INVALID_ARG;
+  if (p->batch < 0 || p->max_kv_len < 0 || p->n_q_heads < 1 || p->n_kv_heads < 1 || p->head_dim < 1 ||
+      p->num_splits < 0)
+    return DIFFATTN_ERR_INVALID_ARG;
+  if (p->variant != DIFFATTN_V1 && p->variant != DIFFATTN_V2) return DIFFATTN_ERR_INVALID_ARG;
+  if (p->dtype != DIFFATTN_BF16)
+    return p->dtype == DIFFATTN_F32 ? DIFFATTN_ERR_UNSUPPORTED : DIFFATTN_ERR_INVALID_ARG;
+  const bool v1 = p->variant == DIFFATTN_V1;
+  if (v1 ? p->n_q_heads != p->n_kv_heads
+         : (p->n_q_heads % p->n_kv_heads != 0 || (p->n_q_heads / p->n_kv_heads) % 2 != 0))
+    return DIFFATTN_ERR_INVALID_ARG;
+  if (p->head_dim != (v1 ? 64 : 128)) return DIFFATTN_ERR_UNSUPPORTED;
+  if (!strides_ok(p->q_strides, 2) || !strides_ok(p->o_strides, 2)) return DIFFATTN_ERR_INVALID_ARG;
+  if (p->batch > 65535 || p->n_q_heads > 65535 || p->max_kv_len > (1 << 30)) return DIFFATTN_ERR_UNSUPPORTED;
+  const int L = p->max_kv_len, group = v1 ? 2 : p->n_q_heads / p->n_kv_heads;
+  int64_t s = p->num_splits ? p->num_splits : decode_kv4_default_splits(p->batch, L, p->n_kv_heads, group);
+  int64_t len = (L + s - 1) / s;
+  len = ((len + kKv4Chunk - 1) / kKv4Chunk) * kKv4Chunk;
+  if (len < kKv4Chunk) len = kKv4Chunk;
+  s = (L + len - 1) / len;
+  if (s < 1) s = 1;
+  if (s > 65535) return DIFFATTN_ERR_UNSUPPORTED;
+  *splits = (int)s;
+  *split_len = (int)len;
+  return DIFFATTN_OK;
+}
+
+// per (b, query row, split): 128 partial outputs, then (max, sum); nothing for one split
+static size_t decode_kv4_records(const diffattn_decode_params* p, int splits) {
+  if (splits == 1) return 0;
+  return (size_t)p->batch * p->n_q_heads * (p->variant == DIFFATTN_V1 ? 2 : 1) * splits;
+}
+
+extern "C" {
+
+int diffattn_kv4_write(const diffattn_kv4_rows* p, const diffattn_paged_kv* pk, const void* k,
+                       const void* v, const int32_t* cu_seqlens, const int32_t* pos, void* cache,
+                       const int32_t* block_table, int* dev_status, void* stream) {
+  return kv4_rows_run(true, p, pk, k, v, cu_seqlens, pos, cache, block_table, dev_status, stream);
+}
+
+int diffattn_kv4_read(const diffattn_kv4_rows* p, const diffattn_paged_kv* pk, const void* cache,
+                      const int32_t* block_table, const int32_t* cu_seqlens, const int32_t* pos,
+                      void* k, void* v, int* dev_status, void* stream) {
+  return kv4_rows_run(false, p, pk, k, v, cu_seqlens, pos, cache, block_table, dev_status, stream);
+}
+
+int diffattn_decode_kv4_workspace_size(const diffattn_decode_params* p, size_t* bytes) {
+  if (!bytes) return DIFFATTN_ERR_INVALID_ARG;
+  int splits = 0, len = 0;
+  const int rc = decode_kv4_check(p, &splits, &len);
+  if (rc != DIFFATTN_OK) return rc;
+  *bytes = decode_kv4_records(p, splits) * 130 * sizeof(float);
+  return DIFFATTN_OK;
+}
+
+int diffattn_fwd_decode_kv4(const diffattn_decode_params* p, const diffattn_paged_kv* pk,
+                            const void* q, const void* cache, const int32_t* block_table,
+                            const int32_t* kv_len, const float* lambda, const float* lambda_init,
+                            int apply_norm, float norm_eps, void* out, void* workspace,
+                            size_t workspace_bytes, int* dev_status, void* stream) {
+  int splits = 0, len = 0;
+  int rc = decode_kv4_check(p, &splits, &len);
+  if (rc != DIFFATTN_OK) return rc;
+  const bool v1 = p->variant == DIFFATTN_V1;
+  if (apply_norm != 0 && apply_norm != 1) return DIFFATTN_ERR_INVALID_ARG;
+  if (!v1 && apply_norm) return DIFFATTN_ERR_INVALID_ARG;  // V2 has no per-head norm
+  if (apply_norm && !(norm_eps >= 0.f && isfinite(norm_eps))) return DIFFATTN_ERR_INVALID_ARG;
+  DecodeKv4Args a;
+  memset(&a, 0, sizeof(a));
+  rc = kv4_cache_setup(pk, p->kv_strides, p->batch, p->n_kv_heads, p->max_kv_len, cache, block_table,
+                       dev_status, &a.cache);
+  if (rc != DIFFATTN_OK) return rc;
+  if (p->batch == 0) return DIFFATTN_OK;
+  if (!q || !lambda || !out || (apply_norm && !lambda_init)) return DIFFATTN_ERR_INVALID_ARG;
+  if (p->max_kv_len > 0 && (!cache || (pk && !block_table))) return DIFFATTN_ERR_INVALID_ARG;
+  const size_t recs = decode_kv4_records(p, splits);
+  if (recs) {
+    if (!workspace || workspace_bytes < recs * 130 * sizeof(float)) return DIFFATTN_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return DIFFATTN_ERR_MISALIGNED;
+  }
+  if (!aligned16(q) || !aligned16(out)) return DIFFATTN_ERR_MISALIGNED;
+  if (p->q_strides[0] % 8 || p->q_strides[1] % 8 || p->o_strides[0] % 8 || p->o_strides[1] % 8)
+    return DIFFATTN_ERR_MISALIGNED;
+  a.B = p->batch;
+  a.Hq = p->n_q_heads;
+  a.H = p->n_kv_heads;
+  a.v1 = v1;
+  a.group = v1 ? 2 : a.Hq / a.H;
+  a.splits = splits;
+  a.split_len = len;
+  memcpy(a.qs, p->q_strides, sizeof(a.qs));
+  memcpy(a.os, p->o_strides, sizeof(a.os));
+  a.q = q;
+  a.kv_len = kv_len;
+  a.lambda = lambda;
+  a.lambda_init = lambda_init;
+  a.apply_norm = apply_norm;
+  a.eps = norm_eps;
+  a.out = out;
+  a.ws_o = static_cast<float*>(workspace);
+  a.ws_ml = a.ws_o + recs * 128;
+  const int64_t qh[3] = {p->q_strides[0], 0, p->q_strides[1]};  // [B, 1, heads, 128]
+  const int64_t oh[3] = {p->o_strides[0], 0, p->o_strides[1]};
+  a.ext_q = extent(a.B, 1, a.Hq, 128, qh);
+  a.ext_out = extent(a.B, 1, v1 ? a.Hq : a.Hq / 2, 128, oh);
+  a.ext_ws_o = (int64_t)(recs * 128);
+  a.ext_ws_ml = (int64_t)(recs * 2);
+  return from_cuda(launch_decode_kv4(a, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,528 @@
+// decode_kv4.cu -- split-KV differential attention decode over a cache held in 4 bits (the
+// record: kv4.cuh), V1 and V2, contiguous and paged.
+//
+// With s the scales and n the nibbles of the records, q one query row of a KV head,
+//   x_t = c sum_g sK[t,g] sum_{i in g} q_i (nK[t,i] - 8),       c = log2(e) / sqrt(d)
+//   O   = sum_t 2^(x_t - M) sV[t,g] (nV[t,:] - 8) / sum_t 2^(x_t - M),
+// and out = O_1 - lambda O_2 for the two branches ("Differential Attention (V2)", The
+// Concept). V1 is the same with two rows for each head: branch 1 is (q_1 | 0) and branch 2
+// (0 | q_2) over the cached row (K_1 | K_2), and the norm and scale follow.
+//
+// One block takes (batch entry, KV head, split of the keys, up to 8 NT query rows). Its four
+// warps work alone, each on 32 keys of every 128: a ring of cp.async stages of its own, its
+// own running maximum, sums and output; the block joins them at the end, a second kernel
+// joins the splits. Products run on mma.sync m16n8k16 in fp16 with fp32 sums, keys (or value
+// channels) as the 16 rows and query rows as the 8 columns:
+//   * Codes go from shared memory to registers by ldmatrix (keys: one 16-byte group of a row
+//     per matrix row, a thread gets 8 channels of one key; values: transposed, a thread gets
+//     4 channels of two neighbouring keys, which is the pair an MMA operand register holds).
+//   * K nibbles are used as fp16 subnormals: n in the low mantissa bits is n 2^-24, the next
+//     nibble 16 n 2^-24 against q / 16, so unpacking is one AND for two channels. The -8 is
+//     the accumulators' start, -8 * 2^-24 sum q: exact up to the fp32 sums, since half the
+//     range is all that cancels.
+//   * V nibbles become n - 8 exactly (0x6400 | n is 1024 + n): an offset left in would cancel
+//     over thousands of keys.
+//   * Scales stay outside the MMAs: a group is two k-steps, its fp32 sums are scaled and
+//     added; for V the probability is multiplied by the scale in fp32 and rounded to fp16
+//     once (2^-12 relative; bf16's 2^-9 would be amplified by the subtraction and V1's norm).
+//     fp16's range is kept by the running maximum: M bounds x + E, E the exponent of the
+//     chunk's largest V scale, so products lie under 2^(kTop + kSlack) = 2^15, and M is
+//     raised only when the bound would be passed. Products under 2^-22 of the largest
+//     probability times the largest scale become subnormal and lose bits.
+//   * q is taken times a power of two per row so that its largest element is in [2^14, 2^15);
+//     fp16 then holds every element above 2^-31 of the largest exactly.
+#include <cuda_fp16.h>
+
+#include "kv4.cuh"
+
+namespace diffattn {
+
+namespace {
+constexpr int W = kKv4Width;
+constexpr int WARPS = 4;
+constexpr int THREADS = WARPS * 32;
+constexpr int KEYS = 32;                            // keys of a warp's chunk
+constexpr int STAGES = 4;
+constexpr int STAGE_BYTES = KEYS * kKv4Record;      // 4608
+constexpr int RING_BYTES = STAGES * STAGE_BYTES;
+constexpr int SMEM_BYTES = WARPS * RING_BYTES;      // 73728
+constexpr float kTop = 8.f;                         // p * scale <= 2^kTop when M is raised ...
+constexpr float kSlack = 7.f;                       // ... and <= 2^(kTop + kSlack) before
+static_assert(kKv4Chunk == WARPS * KEYS, "a block's keys");
+static_assert(W == THREADS, "one thread per value channel in the joins");
+}  // namespace
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// transpose of an 8 x 8 matrix of 16-bit elements held one row per four lanes
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// nibbles 0 (low half) and 4 (high half) of w, minus 8, as fp16; the same of nibbles 1 and 5
+__device__ __forceinline__ uint32_t nibble0_f16(uint32_t w) {
+  const uint32_t x = (w & 0x000f000fu) | 0x64006400u;  // 1024 + n
+  const __half2 y = __hadd2(*reinterpret_cast<const __half2*>(&x), __float2half2_rn(-1032.f));
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
+__device__ __forceinline__ uint32_t nibble1_f16(uint32_t w) {
+  const uint32_t x = (w & 0x00f000f0u) | 0x64006400u;  // 1024 + 16 n
+  const __half2 y = __hfma2(*reinterpret_cast<const __half2*>(&x), __float2half2_rn(0.0625f),
+                            __float2half2_rn(-72.f));
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
+
+// The output of one unit (V1 head or V2 pair) from its branches' attention outputs, channel
+// `c` of W = 128 threads: the difference, and V1's norm and scale. All threads of the block
+// take part; `red` holds 4 floats.
+__device__ __forceinline__ void store_unit(const DecodeKv4Args& a, int b, int u, int c, float o1, float o2,
+                                           float* red) {
+  float y = o1 - __ldg(a.lambda + u) * o2;
+  if (a.apply_norm) {
+    const float ss = warp_sum(y * y);
+    if ((c & 31) == 0) red[c >> 5] = ss;
+    __syncthreads();
+    const float tot = (red[0] + red[1]) + (red[2] + red[3]);
+    __syncthreads();
+    y = y * rsqrtf(tot * (1.f / W) + a.eps) * (1.f - __ldg(a.lambda_init));
+  }
+  const int64_t off = b * a.os[0] + (int64_t)u * a.os[1] + c;
+  if (in_bounds(off, 1, a.ext_out, a.cache.dev_status, a.cache.dbg_status))
+    static_cast<__nv_bfloat16*>(a.out)[off] = __float2bfloat16_rn(y);
+}
+
+template <int NT, bool PAGED>
+__global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) decode_kv4_split_kernel(DecodeKv4Args a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float red[4];
+  const int tiles = (a.group + 8 * NT - 1) / (8 * NT);
+  const int g = blockIdx.x / tiles, row0 = (blockIdx.x % tiles) * 8 * NT;  // KV head, first query row
+  const int split = blockIdx.y, b = blockIdx.z;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int gq = lane >> 2, tq = lane & 3;  // fragment row (or column) and pair index
+
+  // device-side lengths are clamped into [0, L] so a bad value cannot read past the cache
+  const int kv_len = a.kv_len ? min(max(__ldg(a.kv_len + b), 0), a.cache.L) : a.cache.L;
+  const int t_begin = split * a.split_len;
+  const int t_end = min(t_begin + a.split_len, kv_len);
+  const int w_begin = t_begin + warp * KEYS;
+  const int n_chunks = t_end > w_begin ? (t_end - w_begin + kKv4Chunk - 1) / kKv4Chunk : 0;  // of this warp
+
+  uint8_t* ring = smem + warp * RING_BYTES;
+  const int64_t head_off = (int64_t)g * a.cache.stride[2];
+  bool bad_page = false;
+
+  // The copies of chunk c into its stage: eight lanes take the 128 code bytes of a row, four
+  // rows at a time, then lane r the scales of row r. Rows past t_end, and those of a page
+  // outside the pool, become zeros (scale 0, so K and V rows of zeros). Paged: lane r looks
+  // up the page of row r, one chunk ahead of the copies that need it (`ahead`).
+  int64_t ahead = -1;
+  auto lookup = [&](int c) {
+    if constexpr (PAGED) {
+      const int tok = w_begin + c * kKv4Chunk + lane;
+      ahead = -1;
+      if (tok < t_end) {
+        ahead = kv4_page_offset(a.cache, b, tok);
+        bad_page = bad_page || ahead < 0;
+      }
+    }
+  };
+  auto load = [&](int c) {
+    uint8_t* st = ring + (c % STAGES) * STAGE_BYTES;
+    const int tok0 = w_begin + c * kKv4Chunk;
+    const int piece = lane & 7, sub = lane >> 3;
+    auto copy = [&](int row, int64_t row_off, int part) {
+      bool ok = row_off >= 0;
+      const int64_t off = (ok ? row_off : 0) + head_off + part * 16;
+      ok = ok && in_bounds(off, 16, a.cache.ext, a.cache.dev_status, a.cache.dbg_status);
+      cp_async_16(st + row * kKv4Record + part * 16, a.cache.base + (ok ? off : 0), ok ? 16u : 0u);
+    };
+    if constexpr (PAGED) {
+#pragma unroll
+      for (int it = 0; it < KEYS / 4; ++it) {
+        const int row = it * 4 + sub;
+        copy(row, __shfl_sync(0xffffffffu, ahead, row), piece);
+      }
+      copy(lane, ahead, 8);
+    } else {
+      const int64_t entry = b * a.cache.stride[0];
+#pragma unroll
+      for (int it = 0; it < KEYS / 4; ++it) {
+        const int row = it * 4 + sub, tok = tok0 + row;
+        copy(row, tok < t_end ? entry + tok * a.cache.stride[1] : -1, piece);
+      }
+      copy(lane, tok0 + lane < t_end ? entry + (tok0 + lane) * a.cache.stride[1] : -1, 8);
+    }
+  };
+
+  lookup(0);
+#pragma unroll
+  for (int c = 0; c < STAGES - 1; ++c) {
+    if (c < n_chunks) {
+      load(c);
+      lookup(c + 1);
+    }
+    cp_async_commit();
+  }
+
+  // Query fragments (B operands), rows scaled to fp16: for group gr and k-step ks, register 0
+  // holds channels 32 gr + 8 tq + 2 ks + {0, 4}, register 1 the next pair over 16 (the order
+  // in which the nibbles of a word come). Lane column gq; start and factor are per column of
+  // the accumulators, 2 tq and 2 tq + 1.
+  uint32_t qb[NT][8][2];
+  float start[NT][4][2];  // -8 * 2^-24 * sum of the group's q
+  float factor[NT][2];    // accumulated score -> log2 domain
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int row = row0 + nt * 8 + gq;
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
+    int64_t off = b * a.qs[0];
+    if (a.v1) off += (int64_t)g * a.qs[1];  // the branches lie side by side in the head's row
+    else off += ((int64_t)g * a.group + row) * a.qs[1];
+    const bool ok = row < a.group && in_bounds(off, W, a.ext_q, a.cache.dev_status, a.cache.dbg_status);
+    uint4 w[4];
+    float top = 0.f;
+    bool odd = false;  // an infinity or a NaN
+#pragma unroll
+    for (int gr = 0; gr < 4; ++gr) {
+      // V1: row 0 has only groups 0, 1 (branch 1), row 1 only groups 2, 3 (branch 2)
+      const bool mine = ok && (!a.v1 || (gr >> 1) == row);
+      w[gr] = mine ? *reinterpret_cast<const uint4*>(q + off + gr * 32 + tq * 8) : make_uint4(0u, 0u, 0u, 0u);
+      const uint32_t x[4] = {w[gr].x, w[gr].y, w[gr].z, w[gr].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        top = fmaxf(top, fmaxf(fabsf(bf16_low(x[i])), fabsf(bf16_high(x[i]))));
+        odd = odd || (x[i] & 0x7f80u) == 0x7f80u || (x[i] & 0x7f800000u) == 0x7f800000u;
+      }
+    }
+#pragma unroll
+    for (int o = 1; o <= 2; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    // exponent field of the row's largest element -> scale 2^(141 - ex), inverse in `factor`
+    const int ex = (int)(__float_as_uint(top) >> 23);
+    const float up = odd ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)min(268 - ex, 254) << 23);
+    float sums[4];
+#pragma unroll
+    for (int gr = 0; gr < 4; ++gr) {
+      const uint32_t x[4] = {w[gr].x, w[gr].y, w[gr].z, w[gr].w};
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = bf16_low(x[i]) * up;
+        v[2 * i + 1] = bf16_high(x[i]) * up;
+      }
+      float sum = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        qb[nt][2 * gr + ks][0] = pack_f16(v[2 * ks], v[2 * ks + 4]);
+        qb[nt][2 * gr + ks][1] = pack_f16(v[2 * ks + 1] * 0.0625f, v[2 * ks + 5] * 0.0625f);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += v[i];
+#pragma unroll
+      for (int o = 1; o <= 2; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      sums[gr] = sum * (-8.f / 16777216.f);
+    }
+    // 2^24 (nibbles as 2^-24) * 2^(ex - 141) * log2(e) / sqrt(d). Rows with elements past
+    // 2^117 overflow here to infinite scores
+    const float down = ldexpf(1.4426950408889634f * (a.v1 ? 0.125f : 0.08838834764831845f),
+                              24 - 141 + max(ex, 14));
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int from = (2 * tq + j) * 4;  // a lane of column 2 tq + j
+      factor[nt][j] = __shfl_sync(0xffffffffu, down, from);
+#pragma unroll
+      for (int gr = 0; gr < 4; ++gr) start[nt][gr][j] = __shfl_sync(0xffffffffu, sums[gr], from);
+    }
+  }
+
+  float m[NT][2], bias[NT][2], l[NT][2];  // columns 2 tq, 2 tq + 1: M, kTop - M, sum of p
+  float o[NT][4][2][4];                   // [group][tile]: channels 32 g + 4 gq + 2 tile + {0, 1}
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      m[nt][j] = -INFINITY;
+      bias[nt][j] = kTop;
+      l[nt][j] = 0.f;
+    }
+#pragma unroll
+    for (int gr = 0; gr < 4; ++gr)
+#pragma unroll
+      for (int ti = 0; ti < 2; ++ti)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[nt][gr][ti][i] = 0.f;
+  }
+
+  for (int c = 0; c < n_chunks; ++c) {
+    if (c + STAGES - 1 < n_chunks) {
+      load(c + STAGES - 1);
+      lookup(c + STAGES);
+    }
+    cp_async_commit();
+    cp_async_wait<STAGES - 1>();
+    __syncwarp();
+
+    const uint8_t* st = ring + (c % STAGES) * STAGE_BYTES;
+    const uint32_t st32 = smem_u32(st);
+    const int left = t_end - (w_begin + c * kKv4Chunk);  // keys of the chunk that exist
+
+    // exponent bound of the chunk's V scales: |scale| < 2^E for all of them (bf16 bits are
+    // ordered as magnitudes; not below -90, so that rows of zeros do not overflow p)
+    const uint2 vs = *reinterpret_cast<const uint2*>(st + lane * kKv4Record + kKv4Scales + 8);
+    uint32_t big = __vmaxu2(vs.x & 0x7fff7fffu, vs.y & 0x7fff7fffu);
+    big = max(big & 0xffffu, big >> 16);
+    big = __reduce_max_sync(0xffffffffu, big);
+    const float E = fmaxf((float)((int)(big >> 7) - 126), -90.f);
+
+    // scores of 2 x 16 keys: x[.][mt][0, 1] key mt * 16 + gq, [2, 3] key + 8, columns 2tq, +1
+    float x[NT][2][4];
+    uint4 scales[2][2];  // of those keys: {K 0 1, K 2 3, V 0 1, V 2 3}
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        scales[mt][h] =
+            *reinterpret_cast<const uint4*>(st + (mt * 16 + h * 8 + gq) * kKv4Record + kKv4Scales);
+      const uint32_t row = st32 + (mt * 16 + ((lane >> 3) & 1) * 8 + (lane & 7)) * kKv4Record + (lane >> 4) * 16;
+#pragma unroll
+      for (int gp = 0; gp < 2; ++gp) {
+        uint32_t r[4];
+        ldsm4(row + gp * 32, r);
+#pragma unroll
+        for (int gg = 0; gg < 2; ++gg) {
+          const int gr = 2 * gp + gg;
+          const uint32_t lo = r[2 * gg], hi = r[2 * gg + 1], lo8 = lo >> 8, hi8 = hi >> 8;
+          const uint32_t k0 = gp ? scales[mt][0].y : scales[mt][0].x, k1 = gp ? scales[mt][1].y : scales[mt][1].x;
+          const float s0 = gg ? bf16_high(k0) : bf16_low(k0), s1 = gg ? bf16_high(k1) : bf16_low(k1);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float acc[4] = {start[nt][gr][0], start[nt][gr][1], start[nt][gr][0], start[nt][gr][1]};
+            mma_f16(acc, lo & 0x000f000fu, hi & 0x000f000fu, lo & 0x00f000f0u, hi & 0x00f000f0u,
+                    qb[nt][2 * gr][0], qb[nt][2 * gr][1]);
+            mma_f16(acc, lo8 & 0x000f000fu, hi8 & 0x000f000fu, lo8 & 0x00f000f0u, hi8 & 0x00f000f0u,
+                    qb[nt][2 * gr + 1][0], qb[nt][2 * gr + 1][1]);
+            float* xx = x[nt][mt];
+            if (gr == 0) {
+              xx[0] = s0 * acc[0]; xx[1] = s0 * acc[1]; xx[2] = s1 * acc[2]; xx[3] = s1 * acc[3];
+            } else {
+              xx[0] = fmaf(s0, acc[0], xx[0]); xx[1] = fmaf(s0, acc[1], xx[1]);
+              xx[2] = fmaf(s1, acc[2], xx[2]); xx[3] = fmaf(s1, acc[3], xx[3]);
+            }
+          }
+        }
+      }
+    }
+
+    // into the log2 domain; keys past the end get -inf; does any pass the bound?
+    bool raise = false;
+    float top[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[nt][mt][i] *= factor[nt][i & 1];
+      if (left < KEYS) {
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (mt * 16 + (i >> 1) * 8 + gq >= left) x[nt][mt][i] = -INFINITY;
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        top[nt][j] = E + fmaxf(fmaxf(x[nt][0][j], x[nt][0][2 + j]), fmaxf(x[nt][1][j], x[nt][1][2 + j]));
+        raise = raise || top[nt][j] > m[nt][j] + kSlack;
+      }
+    }
+    if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float t = top[nt][j];
+#pragma unroll
+          for (int s = 4; s <= 16; s <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, s));
+          const float mn = fmaxf(m[nt][j], t);
+          const float alpha = m[nt][j] == -INFINITY ? 0.f : ex2(m[nt][j] - mn);
+          m[nt][j] = mn;
+          bias[nt][j] = mn == -INFINITY ? kTop : kTop - mn;
+          l[nt][j] *= alpha;
+#pragma unroll
+          for (int gr = 0; gr < 4; ++gr)
+#pragma unroll
+            for (int ti = 0; ti < 2; ++ti) {
+              o[nt][gr][ti][j] *= alpha;
+              o[nt][gr][ti][2 + j] *= alpha;
+            }
+        }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[nt][mt][i] = ex2(x[nt][mt][i] + bias[nt][i & 1]);
+          l[nt][i & 1] += x[nt][mt][i];
+        }
+
+    // O += (p scale)^T-fragments times V
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+      const uint32_t row = st32 + (mt * 16 + ((lane >> 3) & 1) * 8 + (lane & 7)) * kKv4Record + kKv4VCodes + (lane >> 4) * 16;
+#pragma unroll
+      for (int gp = 0; gp < 2; ++gp) {
+        uint32_t r[4];
+        ldsm4_t(row + gp * 32, r);
+#pragma unroll
+        for (int gg = 0; gg < 2; ++gg) {
+          const int gr = 2 * gp + gg;
+          const uint32_t v0 = gp ? scales[mt][0].w : scales[mt][0].z, v1 = gp ? scales[mt][1].w : scales[mt][1].z;
+          const float s0 = gg ? bf16_high(v0) : bf16_low(v0), s1 = gg ? bf16_high(v1) : bf16_low(v1);
+          const uint32_t lo = r[2 * gg], hi = r[2 * gg + 1], lo8 = lo >> 8, hi8 = hi >> 8;
+          const uint32_t a00 = nibble0_f16(lo), a01 = nibble1_f16(lo), a02 = nibble0_f16(hi), a03 = nibble1_f16(hi);
+          const uint32_t a10 = nibble0_f16(lo8), a11 = nibble1_f16(lo8), a12 = nibble0_f16(hi8), a13 = nibble1_f16(hi8);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float* p = x[nt][mt];
+            const uint32_t b0 = transpose8(pack_f16(p[0] * s0, p[1] * s0));
+            const uint32_t b1 = transpose8(pack_f16(p[2] * s1, p[3] * s1));
+            mma_f16(o[nt][gr][0], a00, a01, a02, a03, b0, b1);
+            mma_f16(o[nt][gr][1], a10, a11, a12, a13, b0, b1);
+          }
+        }
+      }
+    }
+    __syncwarp();  // the stage is refilled by the next iteration's copies
+  }
+  cp_async_wait<0>();
+  if (bad_page) report_status(a.cache.dev_status, DIFFATTN_ERR_INVALID_ARG);
+
+  // join the warps: [warp][row][channel] outputs and their (M, l) in the ring's memory
+  constexpr int ROWS = 8 * NT;
+  float* sm_o = reinterpret_cast<float*>(smem);
+  float* sm_ml = sm_o + WARPS * ROWS * W;
+  static_assert(WARPS * ROWS * (W + 2) * 4 <= SMEM_BYTES, "the join fits in the ring");
+  __syncthreads();
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int row = warp * ROWS + nt * 8 + 2 * tq + j;
+#pragma unroll
+      for (int s = 4; s <= 16; s <<= 1) l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], s);
+      if (gq == 0) {
+        sm_ml[2 * row] = m[nt][j];
+        sm_ml[2 * row + 1] = l[nt][j];
+      }
+#pragma unroll
+      for (int gr = 0; gr < 4; ++gr)
+        *reinterpret_cast<float4*>(sm_o + row * W + gr * 32 + gq * 4) =
+            make_float4(o[nt][gr][0][j], o[nt][gr][0][2 + j], o[nt][gr][1][j], o[nt][gr][1][2 + j]);
+    }
+  __syncthreads();
+  const int rows = min(ROWS, a.group - row0);
+  float prev = 0.f;
+  for (int r = 0; r < rows; ++r) {
+    float M = -INFINITY, L = 0.f, O = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) M = fmaxf(M, sm_ml[2 * (w * ROWS + r)]);
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      const float mw = sm_ml[2 * (w * ROWS + r)];
+      // a warp without keys, or with none above -inf, has M = -inf and nothing to add; only
+      // a NaN among its sums is passed on
+      const float f = mw == -INFINITY ? 1.f : ex2(mw - M);
+      L = fmaf(sm_ml[2 * (w * ROWS + r) + 1], f, L);
+      O = fmaf(sm_o[(w * ROWS + r) * W + tid], f, O);
+    }
+    if (a.splits == 1) {
+      const float y = L == 0.f ? 0.f : O / L;
+      if (r & 1) store_unit(a, b, a.v1 ? g : (g * a.group + row0 + r) >> 1, tid, prev, y, red);
+      prev = y;
+    } else {
+      const int64_t rec = ((int64_t)b * a.H * a.group + g * a.group + row0 + r) * a.splits + split;
+      if (in_bounds(rec * W + tid, 1, a.ext_ws_o, a.cache.dev_status, a.cache.dbg_status))
+        a.ws_o[rec * W + tid] = O;
+      if (tid == 0 && in_bounds(rec * 2, 2, a.ext_ws_ml, a.cache.dev_status, a.cache.dbg_status)) {
+        a.ws_ml[rec * 2] = M;
+        a.ws_ml[rec * 2 + 1] = L;
+      }
+    }
+  }
+}
+
+// One block of 128 threads per unit (V1 head or V2 pair) and batch entry: thread c owns value
+// channel c and joins the splits of the unit's two query rows.
+__global__ void __launch_bounds__(W) decode_kv4_combine_kernel(DecodeKv4Args a) {
+  __shared__ float red[4];
+  const int u = blockIdx.x, b = blockIdx.y, c = threadIdx.x;
+  float res[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int64_t rec0 = ((int64_t)b * a.H * a.group + 2 * u + e) * a.splits;
+    if (!in_bounds(rec0 * 2, 2 * (int64_t)a.splits, a.ext_ws_ml, a.cache.dev_status, a.cache.dbg_status) ||
+        !in_bounds(rec0 * W, (int64_t)a.splits * W, a.ext_ws_o, a.cache.dev_status, a.cache.dbg_status)) {
+      res[e] = 0.f;
+      continue;
+    }
+    float M = -INFINITY, L = 0.f, O = 0.f;
+    for (int s = 0; s < a.splits; ++s) M = fmaxf(M, a.ws_ml[(rec0 + s) * 2]);
+    for (int s = 0; s < a.splits; ++s) {
+      const float ms = a.ws_ml[(rec0 + s) * 2];
+      const float f = ms == -INFINITY ? 1.f : ex2(ms - M);
+      L = fmaf(a.ws_ml[(rec0 + s) * 2 + 1], f, L);
+      O = fmaf(a.ws_o[(rec0 + s) * W + c], f, O);
+    }
+    res[e] = L == 0.f ? 0.f : O / L;
+  }
+  store_unit(a, b, u, c, res[0], res[1], red);
+}
+
+int decode_kv4_default_splits(int B, int L, int H, int group) {
+  const int nt = group > 8 ? 2 : 1;
+  const int64_t units = (int64_t)B * H * ((group + 8 * nt - 1) / (8 * nt));
+  int64_t s = (L + 4095) / 4096;
+  const int64_t blocks = 2 * 148 * (nt == 1 ? 3 : 2);
+  if (units > 0 && units * s < blocks) s = (blocks + units - 1) / units;
+  const int64_t most = (L + kKv4Chunk - 1) / kKv4Chunk;
+  if (s > most) s = most;
+  return s < 1 ? 1 : (int)s;
+}
+
+cudaError_t launch_decode_kv4(const DecodeKv4Args& a, cudaStream_t stream) {
+  const bool paged = a.cache.block_table != nullptr;
+  const int nt = a.group > 8 ? 2 : 1;
+  void (*fn)(DecodeKv4Args) = nt == 1 ? (paged ? decode_kv4_split_kernel<1, true> : decode_kv4_split_kernel<1, false>)
+                                      : (paged ? decode_kv4_split_kernel<2, true> : decode_kv4_split_kernel<2, false>);
+  cudaError_t e = cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  const int tiles = (a.group + 8 * nt - 1) / (8 * nt);
+  fn<<<dim3(a.H * tiles, a.splits, a.B), THREADS, SMEM_BYTES, stream>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || a.splits == 1) return e;
+  decode_kv4_combine_kernel<<<dim3(a.H * a.group / 2, a.B), W, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace diffattn

@@ -134,6 +134,62 @@ struct DecodeArgs {
   int* dbg_status;
 };
 
+// A KV cache held in 4 bits: records of 144 bytes (kv4.cuh), contiguous [B, L, H] or a pool
+// of pages with a block table.
+struct Kv4Cache {
+  uint8_t* base;
+  int64_t stride[3];           // bytes: {batch entry or page, token, head}
+  const int32_t* block_table;  // nullptr: contiguous
+  int64_t bt_stride;           // columns of the block table
+  int page_shift, num_pages;
+  int L;                       // positions of an entry
+  // extents (bytes of the cache, entries of the block table) and status words
+  int64_t ext, ext_bt;
+  int* dev_status;
+  int* dbg_status;
+};
+
+// Rows moved between K, V tensors and a 4-bit cache (diffattn_kv4_write, diffattn_kv4_read)
+struct Kv4RowsArgs {
+  Kv4Cache cache;
+  int B, H;
+  int N;                  // rows of an entry; packed: the most rows of one
+  int total;              // packed: rows of the tensors
+  int f32;                // rows are fp32 (else bf16)
+  const int32_t* cu;      // packed: [B + 1] offsets, else nullptr
+  const int32_t* pos;     // [B] position of each entry's first row, or nullptr for 0
+  void* k;                // read from (write) or written to (read)
+  void* v;
+  int64_t ks[3], vs[3];   // elements: {batch, token, head}
+  int64_t ext_k, ext_v;
+};
+
+// Decode over a 4-bit cache (diffattn_fwd_decode_kv4)
+struct DecodeKv4Args {
+  Kv4Cache cache;
+  int B, Hq, H;           // V1: Hq = H heads of two branches; V2: Hq query heads over H
+  int v1;
+  int group;              // query rows of a KV head: V1 2 (its branches), V2 Hq / H
+  int splits, split_len;  // keys of a split (a multiple of kKv4Chunk)
+  int64_t qs[2], os[2];
+  const void* q;
+  const int32_t* kv_len;
+  const float* lambda;
+  const float* lambda_init;
+  int apply_norm;
+  float eps;
+  void* out;
+  float* ws_o;            // [B, H * group, splits, 128], splits > 1
+  float* ws_ml;           // [B, H * group, splits, 2]
+  int64_t ext_q, ext_out, ext_ws_o, ext_ws_ml;
+};
+
+constexpr int kKv4Chunk = 128;  // keys that a block of the decode takes at a time
+cudaError_t launch_kv4_write(const Kv4RowsArgs& a, cudaStream_t stream);
+cudaError_t launch_kv4_read(const Kv4RowsArgs& a, cudaStream_t stream);
+int decode_kv4_default_splits(int B, int L, int H, int group);
+cudaError_t launch_decode_kv4(const DecodeKv4Args& a, cudaStream_t stream);
+
 cudaError_t launch_lambda(const float* lq1, const float* lk1, const float* lq2, const float* lk2,
                           int n_heads, int dim, int depth, float* lam, float* lam_init,
                           cudaStream_t stream);

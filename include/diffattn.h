@@ -27,7 +27,9 @@
  * diffattn_fwd_decode (V2), diffattn_fwd_decode_v1, diffattn_fwd_decode_paged (block
  * table), diffattn_fwd_decode_static, diffattn_decode_workspace_size; diffattn_bwd_prefill,
  * diffattn_bwd_workspace_size, diffattn_fwd_prefill_train, diffattn_bwd_prefill_saved,
- * diffattn_lambda_bwd (training); diffattn_selftest_timeout
+ * diffattn_lambda_bwd (training); diffattn_kv4_write, diffattn_kv4_read,
+ * diffattn_fwd_decode_kv4, diffattn_decode_kv4_workspace_size (a KV cache held in 4 bits);
+ * diffattn_selftest_timeout
  * (the bounded-wait path), diffattn_selftest_exp2 (the FMA-pipe 2^x),
  * diffattn_debug_bounds_violations (the bounds-checked build); diffattn_version,
  * diffattn_status_string.
@@ -441,6 +443,118 @@ int diffattn_fwd_decode_paged(const diffattn_decode_params* p, const diffattn_pa
 int diffattn_fwd_decode_static(const diffattn_decode_params* p, const void* q,
                                const void* k_cache, const void* v_cache, const int32_t* kv_len,
                                const float* lambda, void* out, int* dev_status, void* stream);
+
+/*
+ * KV cache held in 4 bits. (The pages fix no cache format; they name the cache's size and its
+ * loads as what decode costs -- "Differential Attention (V2)", "V1 vs V2". This cache takes
+ * 144 bytes for a token and KV head where the bf16 one takes 512.)
+ *
+ * One record of DIFFATTN_KV4_RECORD_BYTES for each (token, KV head) holds its K row and its V
+ * row, 128 channels each (V2: d = 128; V1: K_1 | K_2 with d = 64, and V of width 2d), in four
+ * groups of 32 channels:
+ *   bytes   0.. 63  K codes: byte i holds channel 2i in its low and 2i + 1 in its high nibble
+ *   bytes  64..127  V codes, the same
+ *   bytes 128..135  K scales, bf16, one for each group
+ *   bytes 136..143  V scales
+ * A nibble n of group g stands for scale[g] * (n - 8). Writing a group x (bf16; fp32 rows are
+ * rounded to bf16 first): with x* its element of largest magnitude, the negative one where
+ * both signs have it, scale = -x* / 8 (exact in bf16) and n = clamp(rne(x / scale), -8, 7) + 8
+ * (rne: to the nearest integer, ties to even). So x* is held exactly, an element of the other
+ * sign past 7.5 scales is off by at most |scale|, any other by at most |scale| / 2. A group
+ * with |x*| < 2^-100 is held as zeros; one with a NaN or an infinity gets a NaN scale and
+ * reads back as NaN.
+ *
+ * Two layouts, as for the bf16 caches, with strides in BYTES:
+ *   contiguous  [B, L, H] records; strides {batch, token, head}
+ *   paged       a pool [num_pages, page_size, H] of records, pk->page_strides {page, token,
+ *               head}; token t of entry b is row t % page_size of page
+ *               block_table[b][t / page_size] (int32 [B, max_pages_per_seq], row-major)
+ * Cache base 16-byte aligned, byte strides multiples of 16; two records must not overlap.
+ */
+#define DIFFATTN_KV4_RECORD_BYTES 144
+
+/*
+ * Rows moved by diffattn_kv4_write and diffattn_kv4_read. Row i of entry b is position
+ * pos[b] + i of the entry (pos: int32 [B], device; NULL = 0 for all).
+ *   fixed length  cu_seqlens NULL: k [B, N, H, 128], v [B, N, H, 128], N = n_tokens
+ *   packed        cu_seqlens int32 [B + 1], device: entry b owns rows cu_seqlens[b] ..
+ *                 cu_seqlens[b+1] - 1 of k, v [n_tokens, H, 128]; max_seqlen (HOST) >= every
+ *                 entry's count sizes the launch; the batch strides are ignored
+ * (V1: k is [.., H, 2, 64], the same 128 contiguous channels.)
+ * Element strides {batch, token, head}, the 128 channels contiguous; k and v 16-byte aligned,
+ * strides multiples of 8 elements (bf16) or 4 (f32). The rows must not overlap the cache.
+ */
+typedef struct {
+  int32_t dtype;       /* diffattn_dtype of k and v */
+  int32_t batch;       /* B >= 0 (at most 65535) */
+  int32_t n_tokens;    /* rows of each entry; packed: rows in all */
+  int32_t max_seqlen;  /* packed: the most rows of an entry; fixed length: ignored */
+  int32_t n_kv_heads;  /* H */
+  int32_t max_kv_len;  /* L, positions of an entry (at most 2^30) */
+  int64_t k_strides[3];
+  int64_t v_strides[3];
+  int64_t cache_strides[3]; /* bytes; ignored when paged */
+} diffattn_kv4_rows;
+
+/*
+ * diffattn_kv4_write -- quantise rows of K and V into the cache at their positions: a prompt
+ * (pos NULL), a chunk behind earlier tokens, or each entry's newest token (N = 1, pos = the
+ * tokens held before). Every other record is left as it was. kv_len is the caller's to advance.
+ *
+ *   pk, block_table : NULL for a contiguous cache; else the pool geometry (HOST pointer) and
+ *                     the table
+ * A row whose position lies outside [0, max_kv_len), or whose page lies outside the pool, is
+ * not written; an entry whose cu_seqlens are inconsistent (negative or decreasing counts, rows
+ * past n_tokens, more than max_seqlen) is skipped; both write DIFFATTN_ERR_INVALID_ARG to
+ * dev_status. Two rows of one call must not name the same record (entries that share a page
+ * may both be read, not written). No rows launch nothing and return DIFFATTN_OK.
+ */
+int diffattn_kv4_write(const diffattn_kv4_rows* p, const diffattn_paged_kv* pk, const void* k,
+                       const void* v, const int32_t* cu_seqlens, const int32_t* pos, void* cache,
+                       const int32_t* block_table, int* dev_status, void* stream);
+
+/*
+ * diffattn_kv4_read -- the values the cache holds, scale * (n - 8), as rows of K and V: exact
+ * in f32, rounded once to bf16. With pos NULL and N = kv_len, the k and v of a chunked prefill
+ * (diffattn_fwd_prefill with kv_seqlen > seqlen) over tokens that are already cached.
+ * Arguments as for diffattn_kv4_write, with k and v written. A row whose position lies outside
+ * [0, max_kv_len), or whose page lies outside the pool, reads as zeros and is reported through
+ * dev_status; rows of a skipped entry, and rows of k and v that no entry owns, are not written.
+ */
+int diffattn_kv4_read(const diffattn_kv4_rows* p, const diffattn_paged_kv* pk, const void* cache,
+                      const int32_t* block_table, const int32_t* cu_seqlens, const int32_t* pos,
+                      void* k, void* v, int* dev_status, void* stream);
+
+/*
+ * diffattn_fwd_decode_kv4 -- diffattn_fwd_decode (p->variant = DIFFATTN_V2) or
+ * diffattn_fwd_decode_v1 (DIFFATTN_V1) over a cache held in 4 bits: the attention over the
+ * values diffattn_kv4_read gives in f32, reading each record once for all query heads of a KV
+ * head (of up to 16).
+ *   p           : as for those calls, with p->kv_strides the cache's BYTE strides (ignored
+ *                 when paged); V2: d = 128 and any even Hq / Hkv; V1: d = 64; max_kv_len at
+ *                 most 2^30
+ *   pk, block_table : NULL for a contiguous cache; else as for diffattn_fwd_decode_paged
+ *                 (entries for pages past kv_len[b] are never read)
+ *   kv_len      : int32 [B] or NULL (NULL = max_kv_len), clamped to [0, max_kv_len]; 0 gives a
+ *                 zero output row
+ *   lambda_init, apply_norm, norm_eps : V1 as for diffattn_fwd_decode_v1; V2: apply_norm = 0
+ *   workspace   : >= diffattn_decode_kv4_workspace_size(p) bytes, 256-byte aligned (NULL where
+ *                 that is 0); calls sharing a workspace must not overlap in time
+ * Arithmetic: q and the codes are exact MMA operands (q after a power-of-two scaling per row;
+ * elements under 2^-31 of a row's largest lose bits, and rows with elements past 2^117
+ * overflow), scales, sums and softmax statistics in fp32, probability times V scale rounded
+ * once to fp16 (2^-11; products under 2^-22 of the row's largest probability times the
+ * largest V scale lose bits, and with V past 2^100 small probabilities are dropped). No
+ * atomics: results do not depend on scheduling.
+ * A block-table entry outside the pool is handled as by diffattn_fwd_decode_paged. Host-side
+ * errors as for the other decodes.
+ */
+int diffattn_decode_kv4_workspace_size(const diffattn_decode_params* p, size_t* bytes);
+int diffattn_fwd_decode_kv4(const diffattn_decode_params* p, const diffattn_paged_kv* pk,
+                            const void* q, const void* cache, const int32_t* block_table,
+                            const int32_t* kv_len, const float* lambda, const float* lambda_init,
+                            int apply_norm, float norm_eps, void* out, void* workspace,
+                            size_t workspace_bytes, int* dev_status, void* stream);
 
 /*
  * diffattn_selftest_timeout -- exercises the kernels' bounded-wait path on purpose.
