@@ -20,8 +20,10 @@
 //     nibble 16 n 2^-24 against q / 16, so unpacking is one AND for two channels. The -8 is
 //     the accumulators' start, -8 * 2^-24 sum q: exact up to the fp32 sums, since half the
 //     range is all that cancels.
-//   * V nibbles become n - 8 exactly (0x6400 | n is 1024 + n): an offset left in would cancel
-//     over thousands of keys.
+//   * V nibbles become n - 8 exactly (0x6400 | n is 1024 + n). Left as subnormals with the -8
+//     from a second MMA over constants the full step took 455 us instead of 469, but the
+//     cancelling sums lost up to 2^-16 of a scale, which shows where a peaked row's key has
+//     the code 0.
 //   * Scales stay outside the MMAs: a group is two k-steps, its fp32 sums are scaled and
 //     added; for V the probability is multiplied by the scale in fp32 and rounded to fp16
 //     once (2^-12 relative; bf16's 2^-9 would be amplified by the subtraction and V1's norm).
@@ -33,7 +35,10 @@
 //     fp16 then holds every element above 2^-31 of the largest exactly.
 #include <cuda_fp16.h>
 
+#include <string.h>
+
 #include "kv4.cuh"
+#include "tma_host.cuh"
 
 namespace diffattn {
 
@@ -50,6 +55,12 @@ constexpr float kTop = 8.f;                         // p * scale <= 2^kTop when 
 constexpr float kSlack = 7.f;                       // ... and <= 2^(kTop + kSlack) before
 static_assert(kKv4Chunk == WARPS * KEYS, "a block's keys");
 static_assert(W == THREADS, "one thread per value channel in the joins");
+static_assert(STAGE_BYTES % 128 == 0 && (8 * kKv4Record) % 128 == 0, "TMA destinations");
+
+// How a chunk reaches shared memory: TMA boxes of 32 records (contiguous) or of a page's run
+// of up to 32 (pages of 8 tokens and more; a box of fewer would not end on a 128-byte
+// boundary), or 16-byte copies (smaller pages, and strides that TMA does not take).
+enum Kv4Load { kTma, kTmaPaged, kCopy };
 }  // namespace
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -60,35 +71,39 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                        uint32_t b0, uint32_t b1) {
+// d = a b + c
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1, const float (&c)[4]) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      "{%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
+// the even and the odd nibbles of the low byte of each half of w, as fp16: n 2^-24, 16 n 2^-24
+__device__ __forceinline__ uint32_t nib_even(uint32_t w) { return w & 0x000f000fu; }
+__device__ __forceinline__ uint32_t nib_odd(uint32_t w) { return w & 0x00f000f0u; }
 // transpose of an 8 x 8 matrix of 16-bit elements held one row per four lanes
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-// nibbles 0 (low half) and 4 (high half) of w, minus 8, as fp16; the same of nibbles 1 and 5
-__device__ __forceinline__ uint32_t nibble0_f16(uint32_t w) {
-  const uint32_t x = (w & 0x000f000fu) | 0x64006400u;  // 1024 + n
+// the same nibbles minus 8, exact: 1024 + n - 1032 and (1024 + 16 n) / 16 - 72
+__device__ __forceinline__ uint32_t code_even(uint32_t w) {
+  const uint32_t x = (w & 0x000f000fu) | 0x64006400u;
   const __half2 y = __hadd2(*reinterpret_cast<const __half2*>(&x), __float2half2_rn(-1032.f));
   return *reinterpret_cast<const uint32_t*>(&y);
 }
-__device__ __forceinline__ uint32_t nibble1_f16(uint32_t w) {
-  const uint32_t x = (w & 0x00f000f0u) | 0x64006400u;  // 1024 + 16 n
+__device__ __forceinline__ uint32_t code_odd(uint32_t w) {
+  const uint32_t x = (w & 0x00f000f0u) | 0x64006400u;
   const __half2 y = __hfma2(*reinterpret_cast<const __half2*>(&x), __float2half2_rn(0.0625f),
                             __float2half2_rn(-72.f));
   return *reinterpret_cast<const uint32_t*>(&y);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // The output of one unit (V1 head or V2 pair) from its branches' attention outputs, channel
@@ -110,9 +125,28 @@ __device__ __forceinline__ void store_unit(const DecodeKv4Args& a, int b, int u,
     static_cast<__nv_bfloat16*>(a.out)[off] = __float2bfloat16_rn(y);
 }
 
-template <int NT, bool PAGED>
-__global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) decode_kv4_split_kernel(DecodeKv4Args a) {
+// missing[s] = v and missing[s] with the array in registers
+template <int N>
+__device__ __forceinline__ void set_stage(uint32_t (&m)[N], int s, uint32_t v) {
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (i == s) m[i] = v;
+}
+template <int N>
+__device__ __forceinline__ uint32_t get_stage(const uint32_t (&m)[N], int s) {
+  uint32_t v = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (i == s) v = m[i];
+  return v;
+}
+
+template <int NT, Kv4Load LOAD>
+__global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2)
+    decode_kv4_split_kernel(const __grid_constant__ CUtensorMap map, DecodeKv4Args a) {
   extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t landed[WARPS][STAGES];  // TMA: the chunk in a stage has arrived
+  __shared__ int abort_flag;
   __shared__ float red[4];
   const int tiles = (a.group + 8 * NT - 1) / (8 * NT);
   const int g = blockIdx.x / tiles, row0 = (blockIdx.x % tiles) * 8 * NT;  // KV head, first query row
@@ -128,52 +162,85 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) decode_kv4_split_ker
   const int n_chunks = t_end > w_begin ? (t_end - w_begin + kKv4Chunk - 1) / kKv4Chunk : 0;  // of this warp
 
   uint8_t* ring = smem + warp * RING_BYTES;
-  const int64_t head_off = (int64_t)g * a.cache.stride[2];
+  [[maybe_unused]] const int64_t head_off = (int64_t)g * a.cache.stride[2];
   bool bad_page = false;
 
-  // The copies of chunk c into its stage: eight lanes take the 128 code bytes of a row, four
-  // rows at a time, then lane r the scales of row r. Rows past t_end, and those of a page
-  // outside the pool, become zeros (scale 0, so K and V rows of zeros). Paged: lane r looks
-  // up the page of row r, one chunk ahead of the copies that need it (`ahead`).
+  // Paged: the pages of a chunk are looked up one chunk ahead of its copies. kTmaPaged: lane i
+  // holds box i's page; kCopy: lane r the byte offset of record r. -1: no key there, -2:
+  // a page outside the pool. Either way the records' scales become zero, so they count as K
+  // and V rows of zeros (and keys past the end get no weight at all).
+  const int box_rows = LOAD == kTmaPaged ? min(1 << a.cache.page_shift, KEYS) : KEYS;
   int64_t ahead = -1;
   auto lookup = [&](int c) {
-    if constexpr (PAGED) {
-      const int tok = w_begin + c * kKv4Chunk + lane;
-      ahead = -1;
-      if (tok < t_end) {
-        ahead = kv4_page_offset(a.cache, b, tok);
-        bad_page = bad_page || ahead < 0;
+    const int tok0 = w_begin + c * kKv4Chunk;
+    ahead = -1;
+    if constexpr (LOAD == kTmaPaged) {
+      const int tok = tok0 + lane * box_rows;
+      if (lane * box_rows < KEYS && tok < t_end) {
+        const int64_t bi = (int64_t)b * a.cache.bt_stride + (tok >> a.cache.page_shift);
+        int id = -1;
+        if (in_bounds(bi, 1, a.cache.ext_bt, a.cache.dev_status, a.cache.dbg_status))
+          id = __ldg(a.cache.block_table + bi);
+        ahead = (unsigned)id < (unsigned)a.cache.num_pages ? id : -2;
+      }
+    } else if constexpr (LOAD == kCopy) {
+      if (tok0 + lane < t_end) {
+        ahead = kv4_page_offset(a.cache, b, tok0 + lane);
+        if (ahead < 0) ahead = -2;
       }
     }
+    bad_page = bad_page || ahead == -2;
   };
+  // bit s * KEYS.. : rows of the chunk in stage s that a bad page left out
+  uint32_t missing[LOAD == kTma ? 1 : STAGES];
   auto load = [&](int c) {
-    uint8_t* st = ring + (c % STAGES) * STAGE_BYTES;
+    const int s = c % STAGES;
+    uint8_t* st = ring + s * STAGE_BYTES;
     const int tok0 = w_begin + c * kKv4Chunk;
-    const int piece = lane & 7, sub = lane >> 3;
-    auto copy = [&](int row, int64_t row_off, int part) {
-      bool ok = row_off >= 0;
-      const int64_t off = (ok ? row_off : 0) + head_off + part * 16;
-      ok = ok && in_bounds(off, 16, a.cache.ext, a.cache.dev_status, a.cache.dbg_status);
-      cp_async_16(st + row * kKv4Record + part * 16, a.cache.base + (ok ? off : 0), ok ? 16u : 0u);
-    };
-    if constexpr (PAGED) {
+    if constexpr (LOAD == kTma) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&landed[warp][s], STAGE_BYTES);
+        tma_load_4d(st, &map, &landed[warp][s], 0, g, tok0, b);
+      }
+    } else if constexpr (LOAD == kTmaPaged) {
+      const uint32_t boxes = __ballot_sync(0xffffffffu, ahead >= 0);
+      uint32_t bad = __ballot_sync(0xffffffffu, ahead == -2);
+      if (lane == 0) mbar_arrive_expect_tx(&landed[warp][s], __popc(boxes) * box_rows * kKv4Record);
+      __syncwarp();
+      if (ahead >= 0)
+        tma_load_4d(st + lane * box_rows * kKv4Record, &map, &landed[warp][s], 0, g,
+                    (tok0 + lane * box_rows) & ((1 << a.cache.page_shift) - 1), (int)ahead);
+      uint32_t rows = 0;
+      while (bad) {  // a bad box's rows
+        const int i = __ffs(bad) - 1;
+        bad &= bad - 1;
+        rows |= (box_rows == 32 ? 0xffffffffu : (1u << box_rows) - 1u) << (i * box_rows);
+      }
+      set_stage(missing, s, rows);
+    } else {
+      // eight lanes take the 128 code bytes of a record, four records at a time, then lane r
+      // the scales of record r
+      auto copy = [&](int row, int64_t row_off, int part) {
+        bool ok = row_off >= 0;
+        const int64_t off = (ok ? row_off : 0) + head_off + part * 16;
+        ok = ok && in_bounds(off, 16, a.cache.ext, a.cache.dev_status, a.cache.dbg_status);
+        cp_async_16(st + row * kKv4Record + part * 16, a.cache.base + (ok ? off : 0), ok ? 16u : 0u);
+      };
 #pragma unroll
       for (int it = 0; it < KEYS / 4; ++it) {
-        const int row = it * 4 + sub;
-        copy(row, __shfl_sync(0xffffffffu, ahead, row), piece);
+        const int row = it * 4 + (lane >> 3);
+        copy(row, __shfl_sync(0xffffffffu, ahead, row), lane & 7);
       }
       copy(lane, ahead, 8);
-    } else {
-      const int64_t entry = b * a.cache.stride[0];
-#pragma unroll
-      for (int it = 0; it < KEYS / 4; ++it) {
-        const int row = it * 4 + sub, tok = tok0 + row;
-        copy(row, tok < t_end ? entry + tok * a.cache.stride[1] : -1, piece);
-      }
-      copy(lane, tok0 + lane < t_end ? entry + (tok0 + lane) * a.cache.stride[1] : -1, 8);
     }
   };
 
+  if constexpr (LOAD != kCopy) {
+    if (lane < STAGES) mbar_init(&landed[warp][lane], 1);
+    if (tid == 0) abort_flag = 0;
+    fence_barrier_init();
+    __syncthreads();
+  }
   lookup(0);
 #pragma unroll
   for (int c = 0; c < STAGES - 1; ++c) {
@@ -181,7 +248,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) decode_kv4_split_ker
       load(c);
       lookup(c + 1);
     }
-    cp_async_commit();
+    if constexpr (LOAD == kCopy) cp_async_commit();
   }
 
   // Query fragments (B operands), rows scaled to fp16: for group gr and k-step ks, register 0
@@ -189,7 +256,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) decode_kv4_split_ker
   // in which the nibbles of a word come). Lane column gq; start and factor are per column of
   // the accumulators, 2 tq and 2 tq + 1.
   uint32_t qb[NT][8][2];
-  float start[NT][4][2];  // -8 * 2^-24 * sum of the group's q
+  float start[NT][4][4];  // -8 * 2^-24 * sum of the group's q, as accumulators
   float factor[NT][2];    // accumulated score -> log2 domain
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -250,12 +317,14 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) decode_kv4_split_ker
       const int from = (2 * tq + j) * 4;  // a lane of column 2 tq + j
       factor[nt][j] = __shfl_sync(0xffffffffu, down, from);
 #pragma unroll
-      for (int gr = 0; gr < 4; ++gr) start[nt][gr][j] = __shfl_sync(0xffffffffu, sums[gr], from);
+      for (int gr = 0; gr < 4; ++gr)
+        start[nt][gr][j] = start[nt][gr][2 + j] = __shfl_sync(0xffffffffu, sums[gr], from);
     }
   }
 
   float m[NT][2], bias[NT][2], l[NT][2];  // columns 2 tq, 2 tq + 1: M, kTop - M, sum of p
-  float o[NT][4][2][4];                   // [group][tile]: channels 32 g + 4 gq + 2 tile + {0, 1}
+  // [group][tile]: channels 32 g + 4 gq + 2 tile + {0, 1}
+  float o[NT][4][2][4];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -277,13 +346,32 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) decode_kv4_split_ker
       load(c + STAGES - 1);
       lookup(c + STAGES);
     }
-    cp_async_commit();
-    cp_async_wait<STAGES - 1>();
-    __syncwarp();
-
-    const uint8_t* st = ring + (c % STAGES) * STAGE_BYTES;
-    const uint32_t st32 = smem_u32(st);
+    const int stage = c % STAGES;
+    uint8_t* st = ring + stage * STAGE_BYTES;
     const int left = t_end - (w_begin + c * kKv4Chunk);  // keys of the chunk that exist
+    if constexpr (LOAD == kCopy) {
+      cp_async_commit();
+      cp_async_wait<STAGES - 1>();
+      __syncwarp();
+    } else {
+      const bool ok = mbar_wait(&landed[warp][stage], (c / STAGES) & 1, &abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) {
+        // a copy that never landed: let the ones in flight finish before the ring is reused
+        const int issued = min(c + STAGES, n_chunks);
+        for (int cc = c; cc < issued; ++cc) mbar_wait_drain(&landed[warp][cc % STAGES], (cc / STAGES) & 1);
+        if (lane == 0) report_status(a.cache.dev_status, DIFFATTN_ERR_TIMEOUT);
+        break;
+      }
+      uint32_t out = 0;
+      if constexpr (LOAD == kTmaPaged) out = get_stage(missing, stage);
+      if (left < KEYS || out) {  // scales of records that are not there
+        if (lane >= left || ((out >> lane) & 1u))
+          *reinterpret_cast<uint4*>(st + lane * kKv4Record + kKv4Scales) = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async();  // before a later TMA copy rewrites the stage
+        __syncwarp();
+      }
+    }
+    const uint32_t st32 = smem_u32(st);
 
     // exponent bound of the chunk's V scales: |scale| < 2^E for all of them (bf16 bits are
     // ordered as magnitudes; not below -90, so that rows of zeros do not overflow p)
@@ -315,11 +403,11 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) decode_kv4_split_ker
           const float s0 = gg ? bf16_high(k0) : bf16_low(k0), s1 = gg ? bf16_high(k1) : bf16_low(k1);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float acc[4] = {start[nt][gr][0], start[nt][gr][1], start[nt][gr][0], start[nt][gr][1]};
-            mma_f16(acc, lo & 0x000f000fu, hi & 0x000f000fu, lo & 0x00f000f0u, hi & 0x00f000f0u,
-                    qb[nt][2 * gr][0], qb[nt][2 * gr][1]);
-            mma_f16(acc, lo8 & 0x000f000fu, hi8 & 0x000f000fu, lo8 & 0x00f000f0u, hi8 & 0x00f000f0u,
-                    qb[nt][2 * gr + 1][0], qb[nt][2 * gr + 1][1]);
+            float acc[4];
+            mma_f16(acc, nib_even(lo), nib_even(hi), nib_odd(lo), nib_odd(hi), qb[nt][2 * gr][0], qb[nt][2 * gr][1],
+                    start[nt][gr]);
+            mma_f16(acc, nib_even(lo8), nib_even(hi8), nib_odd(lo8), nib_odd(hi8), qb[nt][2 * gr + 1][0],
+                    qb[nt][2 * gr + 1][1], acc);
             float* xx = x[nt][mt];
             if (gr == 0) {
               xx[0] = s0 * acc[0]; xx[1] = s0 * acc[1]; xx[2] = s1 * acc[2]; xx[3] = s1 * acc[3];
@@ -332,15 +420,11 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) decode_kv4_split_ker
       }
     }
 
-    // into the log2 domain; keys past the end get -inf; does any pass the bound?
+    // keys past the end get -inf; does any score pass its row's bound?
     bool raise = false;
     float top[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[nt][mt][i] *= factor[nt][i & 1];
       if (left < KEYS) {
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
@@ -350,7 +434,8 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) decode_kv4_split_ker
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        top[nt][j] = E + fmaxf(fmaxf(x[nt][0][j], x[nt][0][2 + j]), fmaxf(x[nt][1][j], x[nt][1][2 + j]));
+        const float t = fmaxf(fmax3(x[nt][0][j], x[nt][0][2 + j], x[nt][1][j]), x[nt][1][2 + j]);
+        top[nt][j] = fmaf(t, factor[nt][j], E);
         raise = raise || top[nt][j] > m[nt][j] + kSlack;
       }
     }
@@ -382,7 +467,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) decode_kv4_split_ker
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          x[nt][mt][i] = ex2(x[nt][mt][i] + bias[nt][i & 1]);
+          x[nt][mt][i] = ex2(fmaf(x[nt][mt][i], factor[nt][i & 1], bias[nt][i & 1]));
           l[nt][i & 1] += x[nt][mt][i];
         }
 
@@ -400,22 +485,22 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) decode_kv4_split_ker
           const uint32_t v0 = gp ? scales[mt][0].w : scales[mt][0].z, v1 = gp ? scales[mt][1].w : scales[mt][1].z;
           const float s0 = gg ? bf16_high(v0) : bf16_low(v0), s1 = gg ? bf16_high(v1) : bf16_low(v1);
           const uint32_t lo = r[2 * gg], hi = r[2 * gg + 1], lo8 = lo >> 8, hi8 = hi >> 8;
-          const uint32_t a00 = nibble0_f16(lo), a01 = nibble1_f16(lo), a02 = nibble0_f16(hi), a03 = nibble1_f16(hi);
-          const uint32_t a10 = nibble0_f16(lo8), a11 = nibble1_f16(lo8), a12 = nibble0_f16(hi8), a13 = nibble1_f16(hi8);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             const float* p = x[nt][mt];
             const uint32_t b0 = transpose8(pack_f16(p[0] * s0, p[1] * s0));
             const uint32_t b1 = transpose8(pack_f16(p[2] * s1, p[3] * s1));
-            mma_f16(o[nt][gr][0], a00, a01, a02, a03, b0, b1);
-            mma_f16(o[nt][gr][1], a10, a11, a12, a13, b0, b1);
+            float(&o0)[4] = o[nt][gr][0];
+            float(&o1)[4] = o[nt][gr][1];
+            mma_f16(o0, code_even(lo), code_odd(lo), code_even(hi), code_odd(hi), b0, b1, o0);
+            mma_f16(o1, code_even(lo8), code_odd(lo8), code_even(hi8), code_odd(hi8), b0, b1, o1);
           }
         }
       }
     }
     __syncwarp();  // the stage is refilled by the next iteration's copies
   }
-  cp_async_wait<0>();
+  if constexpr (LOAD == kCopy) cp_async_wait<0>();
   if (bad_page) report_status(a.cache.dev_status, DIFFATTN_ERR_INVALID_ARG);
 
   // join the warps: [warp][row][channel] outputs and their (M, l) in the ring's memory
@@ -439,6 +524,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) decode_kv4_split_ker
       for (int gr = 0; gr < 4; ++gr)
         *reinterpret_cast<float4*>(sm_o + row * W + gr * 32 + gq * 4) =
             make_float4(o[nt][gr][0][j], o[nt][gr][0][2 + j], o[nt][gr][1][j], o[nt][gr][1][2 + j]);
+
     }
   __syncthreads();
   const int rows = min(ROWS, a.group - row0);
@@ -510,16 +596,46 @@ int decode_kv4_default_splits(int B, int L, int H, int group) {
   return s < 1 ? 1 : (int)s;
 }
 
-cudaError_t launch_decode_kv4(const DecodeKv4Args& a, cudaStream_t stream) {
+// {144 bytes, heads, rows, entries or pages}, boxes of one head's `box` records; false where
+// the strides are out of TMA's range
+static bool kv4_map(CUtensorMap* m, const Kv4Cache& c, int H, int rows, int outer, int box) {
+  auto fn = encode_fn();
+  if (!fn || rows < 1) return false;
+  int64_t hs = c.stride[2], ts = c.stride[1], os = c.stride[0];
+  // extents of 1 may carry any stride; give TMA a well-formed one
+  if (H == 1) hs = kKv4Record;
+  if (rows == 1) ts = hs * H;
+  if (outer == 1) os = ts * rows;
+  const cuuint64_t dims[4] = {(cuuint64_t)kKv4Record, (cuuint64_t)H, (cuuint64_t)rows, (cuuint64_t)outer};
+  const cuuint64_t strides[3] = {(cuuint64_t)hs, (cuuint64_t)ts, (cuuint64_t)os};
+  const cuuint32_t boxes[4] = {(cuuint32_t)kKv4Record, 1, (cuuint32_t)box, 1};
+  const cuuint32_t steps[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, c.base, dims, strides, boxes, steps,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NT>
+static cudaError_t launch_split(const DecodeKv4Args& a, cudaStream_t stream) {
   const bool paged = a.cache.block_table != nullptr;
-  const int nt = a.group > 8 ? 2 : 1;
-  void (*fn)(DecodeKv4Args) = nt == 1 ? (paged ? decode_kv4_split_kernel<1, true> : decode_kv4_split_kernel<1, false>)
-                                      : (paged ? decode_kv4_split_kernel<2, true> : decode_kv4_split_kernel<2, false>);
+  const int page = 1 << a.cache.page_shift;
+  CUtensorMap map;
+  memset(&map, 0, sizeof(map));
+  void (*fn)(CUtensorMap, DecodeKv4Args) = decode_kv4_split_kernel<NT, kCopy>;
+  if (!paged && kv4_map(&map, a.cache, a.H, a.cache.L, a.B, KEYS)) {
+    fn = decode_kv4_split_kernel<NT, kTma>;
+  } else if (paged && page >= 8 && kv4_map(&map, a.cache, a.H, page, a.cache.num_pages, page < KEYS ? page : KEYS)) {
+    fn = decode_kv4_split_kernel<NT, kTmaPaged>;
+  }
   cudaError_t e = cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  const int tiles = (a.group + 8 * nt - 1) / (8 * nt);
-  fn<<<dim3(a.H * tiles, a.splits, a.B), THREADS, SMEM_BYTES, stream>>>(a);
-  e = cudaGetLastError();
+  const int tiles = (a.group + 8 * NT - 1) / (8 * NT);
+  fn<<<dim3(a.H * tiles, a.splits, a.B), THREADS, SMEM_BYTES, stream>>>(map, a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_decode_kv4(const DecodeKv4Args& a, cudaStream_t stream) {
+  const cudaError_t e = a.group > 8 ? launch_split<2>(a, stream) : launch_split<1>(a, stream);
   if (e != cudaSuccess || a.splits == 1) return e;
   decode_kv4_combine_kernel<<<dim3(a.H * a.group / 2, a.B), W, 0, stream>>>(a);
   return cudaGetLastError();
