@@ -107,21 +107,21 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 }
 
 // The output of one unit (V1 head or V2 pair) from its branches' attention outputs, channel
-// `c` of W = 128 threads: the difference, and V1's norm and scale. All threads of the block
-// take part; `red` holds 4 floats.
-__device__ __forceinline__ void store_unit(const DecodeKv4Args& a, int b, int u, int c, float o1, float o2,
-                                           float* red) {
+// `c` of the W threads with `mine`: the difference, and V1's norm and scale. All threads of the
+// block take part; `red` holds 4 floats.
+__device__ __forceinline__ void store_unit(const DecodeKv4Args& a, int b, int u, int c, bool mine, float o1,
+                                           float o2, float* red) {
   float y = o1 - __ldg(a.lambda + u) * o2;
   if (a.apply_norm) {
     const float ss = warp_sum(y * y);
-    if ((c & 31) == 0) red[c >> 5] = ss;
+    if (mine && (c & 31) == 0) red[c >> 5] = ss;
     __syncthreads();
     const float tot = (red[0] + red[1]) + (red[2] + red[3]);
     __syncthreads();
     y = y * rsqrtf(tot * (1.f / W) + a.eps) * (1.f - __ldg(a.lambda_init));
   }
   const int64_t off = b * a.os[0] + (int64_t)u * a.os[1] + c;
-  if (in_bounds(off, 1, a.ext_out, a.cache.dev_status, a.cache.dbg_status))
+  if (mine && in_bounds(off, 1, a.ext_out, a.cache.dev_status, a.cache.dbg_status))
     static_cast<__nv_bfloat16*>(a.out)[off] = __float2bfloat16_rn(y);
 }
 
@@ -235,6 +235,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2)
     }
   };
 
+  if (a.splits > 1) cudaTriggerProgrammaticLaunchCompletion();
   if constexpr (LOAD != kCopy) {
     if (lane < STAGES) mbar_init(&landed[warp][lane], 1);
     if (tid == 0) abort_flag = 0;
@@ -544,7 +545,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2)
     }
     if (a.splits == 1) {
       const float y = L == 0.f ? 0.f : O / L;
-      if (r & 1) store_unit(a, b, a.v1 ? g : (g * a.group + row0 + r) >> 1, tid, prev, y, red);
+      if (r & 1) store_unit(a, b, a.v1 ? g : (g * a.group + row0 + r) >> 1, tid, true, prev, y, red);
       prev = y;
     } else {
       const int64_t rec = ((int64_t)b * a.H * a.group + g * a.group + row0 + r) * a.splits + split;
@@ -558,42 +559,98 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2)
   }
 }
 
-// One block of 128 threads per unit (V1 head or V2 pair) and batch entry: thread c owns value
-// channel c and joins the splits of the unit's two query rows.
-__global__ void __launch_bounds__(W) decode_kv4_combine_kernel(DecodeKv4Args a) {
-  __shared__ float red[4];
-  const int u = blockIdx.x, b = blockIdx.y, c = threadIdx.x;
+// Joins the splits: one block per unit (V1 head or V2 pair) and batch entry. A split's weight
+// 2^(M_s - M) is computed once by one thread; SLICES threads per value channel then add every
+// SLICES-th split, both rows, and their sums are added in order. (With one thread per channel
+// walking all splits the join of 103 splits took 52 us, more than the attention.)
+constexpr int SLICES = 4;
+constexpr int JOIN = 128;  // splits whose weights are held at a time
+__global__ void __launch_bounds__(W * SLICES) decode_kv4_combine_kernel(DecodeKv4Args a) {
+  __shared__ float weight[2][JOIN];
+  __shared__ float part[SLICES][2][W];
+  __shared__ float red[2][W * SLICES / 32];
+  const int u = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, c = tid % W, slice = tid / W;
+  const int64_t rec0 = ((int64_t)b * a.H * a.group + 2 * u) * a.splits;  // row 2u; row 2u + 1 follows
+  cudaGridDependencySynchronize();  // the split kernel's states
+  const bool ok =
+      in_bounds(rec0 * 2, 4 * (int64_t)a.splits, a.ext_ws_ml, a.cache.dev_status, a.cache.dbg_status) &&
+      in_bounds(rec0 * W, 2 * (int64_t)a.splits * W, a.ext_ws_o, a.cache.dev_status, a.cache.dbg_status);
+  const int splits = ok ? a.splits : 0;
+  const float* ml = a.ws_ml + rec0 * 2;
+  const float* po = a.ws_o + rec0 * W + c;
+
+  float M[2] = {-INFINITY, -INFINITY};
+  for (int s = tid; s < splits; s += W * SLICES)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) M[e] = fmaxf(M[e], ml[2 * (e * splits + s)]);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    M[e] = warp_max(M[e]);
+    if ((tid & 31) == 0) red[e][tid >> 5] = M[e];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+#pragma unroll
+    for (int w = 0; w < W * SLICES / 32; ++w) M[e] = fmaxf(M[e], red[e][w]);
+
+  float L = 0.f, O[2] = {0.f, 0.f};  // threads 0 .. 2 JOIN - 1: row tid / JOIN's sums
+  for (int s0 = 0; s0 < splits; s0 += JOIN) {
+    const int n = min(JOIN, splits - s0);
+    __syncthreads();
+    if (tid < 2 * JOIN && tid % JOIN < n) {
+      const int e = tid / JOIN, s = tid % JOIN;
+      const float2 v = *reinterpret_cast<const float2*>(ml + 2 * (e * splits + s0 + s));
+      // a split without keys has M = -inf and nothing to add; only a NaN is passed on
+      const float f = v.x == -INFINITY ? 1.f : ex2(v.x - (e ? M[1] : M[0]));
+      weight[e][s] = f;
+      L = fmaf(v.y, f, L);
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int s = slice; s < n; s += SLICES) {
+      O[0] = fmaf(po[(int64_t)(s0 + s) * W], weight[0][s], O[0]);
+      O[1] = fmaf(po[(int64_t)(splits + s0 + s) * W], weight[1][s], O[1]);
+    }
+  }
+  L = warp_sum(L);
+  __syncthreads();
+  if ((tid & 31) == 0) red[0][tid >> 5] = L;
+  part[slice][0][c] = O[0];
+  part[slice][1][c] = O[1];
+  __syncthreads();
   float res[2];
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
-    const int64_t rec0 = ((int64_t)b * a.H * a.group + 2 * u + e) * a.splits;
-    if (!in_bounds(rec0 * 2, 2 * (int64_t)a.splits, a.ext_ws_ml, a.cache.dev_status, a.cache.dbg_status) ||
-        !in_bounds(rec0 * W, (int64_t)a.splits * W, a.ext_ws_o, a.cache.dev_status, a.cache.dbg_status)) {
-      res[e] = 0.f;
-      continue;
-    }
-    float M = -INFINITY, L = 0.f, O = 0.f;
-    for (int s = 0; s < a.splits; ++s) M = fmaxf(M, a.ws_ml[(rec0 + s) * 2]);
-    for (int s = 0; s < a.splits; ++s) {
-      const float ms = a.ws_ml[(rec0 + s) * 2];
-      const float f = ms == -INFINITY ? 1.f : ex2(ms - M);
-      L = fmaf(a.ws_ml[(rec0 + s) * 2 + 1], f, L);
-      O = fmaf(a.ws_o[(rec0 + s) * W + c], f, O);
-    }
-    res[e] = L == 0.f ? 0.f : O / L;
+    float l = 0.f, o = 0.f;
+#pragma unroll
+    for (int w = 0; w < JOIN / 32; ++w) l += red[0][e * (JOIN / 32) + w];
+#pragma unroll
+    for (int i = 0; i < SLICES; ++i) o += part[i][e][c];
+    res[e] = l == 0.f ? 0.f : o / l;
   }
-  store_unit(a, b, u, c, res[0], res[1], red);
+  store_unit(a, b, u, c, slice == 0, res[0], res[1], red[1]);
 }
 
+// Splits of the keys: the count whose waves over the GPU's block slots take the least time, a
+// block costing its keys and kSetup more for its start and join.
 int decode_kv4_default_splits(int B, int L, int H, int group) {
   const int nt = group > 8 ? 2 : 1;
   const int64_t units = (int64_t)B * H * ((group + 8 * nt - 1) / (8 * nt));
-  int64_t s = (L + 4095) / 4096;
-  const int64_t blocks = 2 * 148 * (nt == 1 ? 3 : 2);
-  if (units > 0 && units * s < blocks) s = (blocks + units - 1) / units;
-  const int64_t most = (L + kKv4Chunk - 1) / kKv4Chunk;
-  if (s > most) s = most;
-  return s < 1 ? 1 : (int)s;
+  const int64_t slots = 148 * (nt == 1 ? 3 : 2);
+  const int64_t chunks = (L + kKv4Chunk - 1) / kKv4Chunk;
+  const int64_t most = chunks < 256 ? chunks : 256;
+  constexpr int64_t kSetup = 3;  // chunks
+  int64_t best = 1, best_cost = -1;
+  for (int64_t s = 1; s <= most; ++s) {
+    const int64_t waves = (units * s + slots - 1) / slots;
+    const int64_t cost = waves * ((chunks + s - 1) / s + kSetup) + (s > 1 ? 2 : 0);
+    if (best_cost < 0 || cost < best_cost) {
+      best = s;
+      best_cost = cost;
+    }
+  }
+  return (int)best;
 }
 
 // {144 bytes, heads, rows, entries or pages}, boxes of one head's `box` records; false where
@@ -637,8 +694,18 @@ static cudaError_t launch_split(const DecodeKv4Args& a, cudaStream_t stream) {
 cudaError_t launch_decode_kv4(const DecodeKv4Args& a, cudaStream_t stream) {
   const cudaError_t e = a.group > 8 ? launch_split<2>(a, stream) : launch_split<1>(a, stream);
   if (e != cudaSuccess || a.splits == 1) return e;
-  decode_kv4_combine_kernel<<<dim3(a.H * a.group / 2, a.B), W, 0, stream>>>(a);
-  return cudaGetLastError();
+  // launched while the last splits still run; the kernel waits for them itself
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(a.H * a.group / 2, a.B);
+  cfg.blockDim = dim3(W * SLICES);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, decode_kv4_combine_kernel, a);
 }
 
 }  // namespace diffattn
