@@ -182,7 +182,7 @@ def load_library():
     lib.diffattn_kv4_read.restype = i32
     lib.diffattn_kv4_read.argtypes = [ctypes.POINTER(Kv4Rows), vp, vp, vp, vp, vp, vp, vp, vp, vp]
     lib.diffattn_decode_kv4_workspace_size.restype = i32
-    lib.diffattn_decode_kv4_workspace_size.argtypes = [ctypes.POINTER(DecodeParams),
+    lib.diffattn_decode_kv4_workspace_size.argtypes = [ctypes.POINTER(DecodeParams), vp,
                                                        ctypes.POINTER(ctypes.c_size_t)]
     lib.diffattn_fwd_decode_kv4.restype = i32
     lib.diffattn_fwd_decode_kv4.argtypes = [ctypes.POINTER(DecodeParams), vp, vp, vp, vp, vp, f32p, f32p,
@@ -773,10 +773,11 @@ def decode_kv4_params(q, cache, out, num_splits=0, block_table=None, max_kv_len=
     return p, pk
 
 
-def diffattn_decode_kv4_workspace_size(p: DecodeParams) -> int:
+def diffattn_decode_kv4_workspace_size(p: DecodeParams, pk=None) -> int:
     n = ctypes.c_size_t(0)
     _check("diffattn_decode_kv4_workspace_size",
-           load_library().diffattn_decode_kv4_workspace_size(ctypes.byref(p), ctypes.byref(n)))
+           load_library().diffattn_decode_kv4_workspace_size(
+               ctypes.byref(p), None if pk is None else ctypes.byref(pk), ctypes.byref(n)))
     return int(n.value)
 
 
@@ -804,7 +805,7 @@ def diffattn_fwd_decode_kv4(q, cache, lam, kv_len=None, lambda_init=None, out=No
         _kv4_tensor(fn, "out", out, torch.bfloat16, device, (p.batch, units, 128), dense=False)
         if out.stride(-1) != 1:
             _kv4_fail(fn, "the channels of out must be contiguous")
-    need = diffattn_decode_kv4_workspace_size(p)
+    need = diffattn_decode_kv4_workspace_size(p, pk)
     with _kv4_scope(device, stream):
         if out is None:
             out = torch.empty((p.batch, units, 128), dtype=torch.bfloat16, device=device)

@@ -661,7 +661,11 @@ static int kv4_rows_run(bool write, const diffattn_kv4_rows* p, const diffattn_p
   return from_cuda(write ? launch_kv4_write(a, s) : launch_kv4_read(a, s));
 }
 
-static int decode_kv4_check(const diffattn_decode_params* p, int* splits, int* split_len) {
+// Checks everything of a decode that does not need its pointers (cache and pk's table aside)
+// and fills what follows from it.
+static int decode_kv4_setup(const diffattn_decode_params* p, const diffattn_paged_kv* pk, const void* cache,
+                            const int32_t* block_table, int* dev_status, DecodeKv4Args* a) {
+  memset(a, 0, sizeof(*a));
   if (!p) return DIFFATTN_ERR_INVALID_ARG;
   if (p->batch < 0 || p->max_kv_len < 0 || p->n_q_heads < 1 || p->n_kv_heads < 1 || p->head_dim < 1 ||
       p->num_splits < 0)
@@ -676,23 +680,18 @@ static int decode_kv4_check(const diffattn_decode_params* p, int* splits, int* s
   if (p->head_dim != (v1 ? 64 : 128)) return DIFFATTN_ERR_UNSUPPORTED;
   if (!strides_ok(p->q_strides, 2) || !strides_ok(p->o_strides, 2)) return DIFFATTN_ERR_INVALID_ARG;
   if (p->batch > 65535 || p->n_q_heads > 65535 || p->max_kv_len > (1 << 30)) return DIFFATTN_ERR_UNSUPPORTED;
-  const int L = p->max_kv_len, group = v1 ? 2 : p->n_q_heads / p->n_kv_heads;
-  int64_t s = p->num_splits ? p->num_splits : decode_kv4_default_splits(p->batch, L, p->n_kv_heads, group);
-  int64_t len = (L + s - 1) / s;
-  len = ((len + kKv4Chunk - 1) / kKv4Chunk) * kKv4Chunk;
-  if (len < kKv4Chunk) len = kKv4Chunk;
-  s = (L + len - 1) / len;
-  if (s < 1) s = 1;
-  if (s > 65535) return DIFFATTN_ERR_UNSUPPORTED;
-  *splits = (int)s;
-  *split_len = (int)len;
+  const int rc = kv4_cache_setup(pk, p->kv_strides, p->batch, p->n_kv_heads, p->max_kv_len, cache, block_table,
+                                 dev_status, &a->cache);
+  if (rc != DIFFATTN_OK) return rc;
+  a->B = p->batch;
+  a->Hq = p->n_q_heads;
+  a->H = p->n_kv_heads;
+  a->v1 = v1;
+  a->group = v1 ? 2 : a->Hq / a->H;
+  decode_kv4_plan(a, p->num_splits);
+  // 32-bit chunk numbers and grid
+  if (a->chunks > INT32_MAX || a->blocks > INT32_MAX) return DIFFATTN_ERR_UNSUPPORTED;
   return DIFFATTN_OK;
-}
-
-// per (b, query row, split): 128 partial outputs, then (max, sum); nothing for one split
-static size_t decode_kv4_records(const diffattn_decode_params* p, int splits) {
-  if (splits == 1) return 0;
-  return (size_t)p->batch * p->n_q_heads * (p->variant == DIFFATTN_V1 ? 2 : 1) * splits;
 }
 
 extern "C" {
@@ -709,12 +708,13 @@ int diffattn_kv4_read(const diffattn_kv4_rows* p, const diffattn_paged_kv* pk, c
   return kv4_rows_run(false, p, pk, k, v, cu_seqlens, pos, cache, block_table, dev_status, stream);
 }
 
-int diffattn_decode_kv4_workspace_size(const diffattn_decode_params* p, size_t* bytes) {
+int diffattn_decode_kv4_workspace_size(const diffattn_decode_params* p, const diffattn_paged_kv* pk,
+                                       size_t* bytes) {
   if (!bytes) return DIFFATTN_ERR_INVALID_ARG;
-  int splits = 0, len = 0;
-  const int rc = decode_kv4_check(p, &splits, &len);
+  DecodeKv4Args a;
+  const int rc = decode_kv4_setup(p, pk, nullptr, nullptr, nullptr, &a);
   if (rc != DIFFATTN_OK) return rc;
-  *bytes = decode_kv4_records(p, splits) * 130 * sizeof(float);
+  *bytes = a.B ? (size_t)a.states * 130 * sizeof(float) : 0;
   return DIFFATTN_OK;
 }
 
@@ -723,36 +723,21 @@ int diffattn_fwd_decode_kv4(const diffattn_decode_params* p, const diffattn_page
                             const int32_t* kv_len, const float* lambda, const float* lambda_init,
                             int apply_norm, float norm_eps, void* out, void* workspace,
                             size_t workspace_bytes, int* dev_status, void* stream) {
-  int splits = 0, len = 0;
-  int rc = decode_kv4_check(p, &splits, &len);
+  DecodeKv4Args a;
+  const int rc = decode_kv4_setup(p, pk, cache, block_table, dev_status, &a);
   if (rc != DIFFATTN_OK) return rc;
-  const bool v1 = p->variant == DIFFATTN_V1;
+  const bool v1 = a.v1;
   if (apply_norm != 0 && apply_norm != 1) return DIFFATTN_ERR_INVALID_ARG;
   if (!v1 && apply_norm) return DIFFATTN_ERR_INVALID_ARG;  // V2 has no per-head norm
   if (apply_norm && !(norm_eps >= 0.f && isfinite(norm_eps))) return DIFFATTN_ERR_INVALID_ARG;
-  DecodeKv4Args a;
-  memset(&a, 0, sizeof(a));
-  rc = kv4_cache_setup(pk, p->kv_strides, p->batch, p->n_kv_heads, p->max_kv_len, cache, block_table,
-                       dev_status, &a.cache);
-  if (rc != DIFFATTN_OK) return rc;
   if (p->batch == 0) return DIFFATTN_OK;
   if (!q || !lambda || !out || (apply_norm && !lambda_init)) return DIFFATTN_ERR_INVALID_ARG;
   if (p->max_kv_len > 0 && (!cache || (pk && !block_table))) return DIFFATTN_ERR_INVALID_ARG;
-  const size_t recs = decode_kv4_records(p, splits);
-  if (recs) {
-    if (!workspace || workspace_bytes < recs * 130 * sizeof(float)) return DIFFATTN_ERR_WORKSPACE;
-    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return DIFFATTN_ERR_MISALIGNED;
-  }
+  if (!workspace || workspace_bytes < (size_t)a.states * 130 * sizeof(float)) return DIFFATTN_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return DIFFATTN_ERR_MISALIGNED;
   if (!aligned16(q) || !aligned16(out)) return DIFFATTN_ERR_MISALIGNED;
   if (p->q_strides[0] % 8 || p->q_strides[1] % 8 || p->o_strides[0] % 8 || p->o_strides[1] % 8)
     return DIFFATTN_ERR_MISALIGNED;
-  a.B = p->batch;
-  a.Hq = p->n_q_heads;
-  a.H = p->n_kv_heads;
-  a.v1 = v1;
-  a.group = v1 ? 2 : a.Hq / a.H;
-  a.splits = splits;
-  a.split_len = len;
   memcpy(a.qs, p->q_strides, sizeof(a.qs));
   memcpy(a.os, p->o_strides, sizeof(a.os));
   a.q = q;
@@ -763,13 +748,13 @@ int diffattn_fwd_decode_kv4(const diffattn_decode_params* p, const diffattn_page
   a.eps = norm_eps;
   a.out = out;
   a.ws_o = static_cast<float*>(workspace);
-  a.ws_ml = a.ws_o + recs * 128;
+  a.ws_ml = a.ws_o + a.states * 128;
   const int64_t qh[3] = {p->q_strides[0], 0, p->q_strides[1]};  // [B, 1, heads, 128]
   const int64_t oh[3] = {p->o_strides[0], 0, p->o_strides[1]};
   a.ext_q = extent(a.B, 1, a.Hq, 128, qh);
   a.ext_out = extent(a.B, 1, v1 ? a.Hq : a.Hq / 2, 128, oh);
-  a.ext_ws_o = (int64_t)(recs * 128);
-  a.ext_ws_ml = (int64_t)(recs * 2);
+  a.ext_ws_o = a.states * 128;
+  a.ext_ws_ml = a.states * 2;
   return from_cuda(launch_decode_kv4(a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -532,14 +532,17 @@ int diffattn_kv4_read(const diffattn_kv4_rows* p, const diffattn_paged_kv* pk, c
  * head (of up to 16).
  *   p           : as for those calls, with p->kv_strides the cache's BYTE strides (ignored
  *                 when paged); V2: d = 128 and any even Hq / Hkv; V1: d = 64; max_kv_len at
- *                 most 2^30
+ *                 most 2^30; num_splits the parts the keys of an entry are cut into on
+ *                 average, 0 = chosen by the library. The parts have the same number of keys,
+ *                 whatever the entries' lengths
  *   pk, block_table : NULL for a contiguous cache; else as for diffattn_fwd_decode_paged
  *                 (entries for pages past kv_len[b] are never read)
  *   kv_len      : int32 [B] or NULL (NULL = max_kv_len), clamped to [0, max_kv_len]; 0 gives a
  *                 zero output row
  *   lambda_init, apply_norm, norm_eps : V1 as for diffattn_fwd_decode_v1; V2: apply_norm = 0
- *   workspace   : >= diffattn_decode_kv4_workspace_size(p) bytes, 256-byte aligned (NULL where
- *                 that is 0); calls sharing a workspace must not overlap in time
+ *   workspace   : >= diffattn_decode_kv4_workspace_size(p, pk) bytes, 256-byte aligned; calls
+ *                 sharing a workspace must not overlap in time. Its size does not grow with
+ *                 the lengths (at most 20 MB with num_splits = 0)
  * Arithmetic: q and the codes are exact MMA operands (q after a power-of-two scaling per row;
  * elements under 2^-31 of a row's largest lose bits, and rows with elements past 2^117
  * overflow), scales, sums and softmax statistics in fp32, probability times V scale rounded
@@ -549,7 +552,8 @@ int diffattn_kv4_read(const diffattn_kv4_rows* p, const diffattn_paged_kv* pk, c
  * A block-table entry outside the pool is handled as by diffattn_fwd_decode_paged. Host-side
  * errors as for the other decodes.
  */
-int diffattn_decode_kv4_workspace_size(const diffattn_decode_params* p, size_t* bytes);
+int diffattn_decode_kv4_workspace_size(const diffattn_decode_params* p, const diffattn_paged_kv* pk,
+                                       size_t* bytes);
 int diffattn_fwd_decode_kv4(const diffattn_decode_params* p, const diffattn_paged_kv* pk,
                             const void* q, const void* cache, const int32_t* block_table,
                             const int32_t* kv_len, const float* lambda, const float* lambda_init,

@@ -369,6 +369,27 @@ def test_decode_rising_scores():
     _check_decode(2, c, rec, q, qx, np.full(4, 0.6, np.float32), [L], num_splits=1)
 
 
+def test_decode_equal_large_scores():
+    """Keys that are all the same have the same score however large, so every output is the
+    plain mean of V: nothing but fp16's rounding of the weights (2^-11 each) and the result's
+    (2^-8) is allowed, whichever warps and blocks held the keys."""
+    rng = _rng(23)
+    L = 1500
+    for size in (1.0, 300.0, 1e5):
+        kx = plain.bf16_round(np.broadcast_to(rng.standard_normal(128), (1, L, 2, 128)).copy() * size)
+        vx = plain.bf16_round(rng.standard_normal((1, L, 2, 128)) + 1.0)
+        rec = plain.records(kx, vx)
+        held = plain.values(rec)[1]
+        qx = plain.bf16_round(np.repeat(kx[0, 0], 8, 0)[None] / size)
+        for page, splits in ((0, 0), (0, 1), (0, 5), (2, 3)):
+            c = Cache(1, L, 2, page, seed=1).set_entries(rec)
+            out = da.diffattn_fwd_decode_kv4(torch.from_numpy(qx).cuda().bfloat16(), c.t, torch.zeros(8, device="cuda"),
+                                             num_splits=splits, **c.where).double().cpu().numpy()
+            ref = np.repeat(held[0].mean(0), 4, 0)
+            allowed = 2.0 ** -10 * np.repeat(np.abs(held[0]).mean(0), 4, 0)
+            assert (np.abs(out[0] - ref) <= allowed + 2.0 ** -8 * (np.abs(ref) + allowed)).all(), (size, page, splits)
+
+
 def test_decode_equal_branches_cancel_exactly():
     case = list(_decode_case(2, 2, 8, 2, 300, [300, 171], seed=12))
     case[2] = case[2].view(2, 4, 2, 128)[:, :, :1].expand(-1, -1, 2, -1).reshape(2, 8, 128).contiguous()
@@ -414,8 +435,10 @@ def test_decode_lengths_outside_are_clamped():
     assert (np.abs(out.double().cpu().numpy() - ref) <= bound).all()
 
 
-def test_decode_strided_and_layouts_agree():
-    """q and out as slices, the cache with the heads outermost or paged: bit-identical."""
+def test_decode_strided_and_layouts():
+    """q and out as slices; pages of 8 tokens and more give the contiguous cache's result bit
+    for bit; smaller pages, and a cache with the heads outermost, go other ways through the
+    kernel and stay within the bound."""
     lens = [300, 123]
     c, rec, q, qx, lam = _decode_case(2, 2, 16, 2, 300, lens, seed=16)
     kw = dict(kv_len=_i32(lens), num_splits=3)
@@ -424,12 +447,31 @@ def test_decode_strided_and_layouts_agree():
     wide = torch.zeros((2, 20, 3, 128), dtype=torch.bfloat16, device="cuda")
     wide[:, 2:18, 1] = q
     out = torch.full((2, 8, 2, 128), 9.0, dtype=torch.bfloat16, device="cuda")
-    hm = Cache(2, 300, 2, head_major=True).set_entries(rec)
-    da.diffattn_fwd_decode_kv4(wide[:, 2:18, 1], hm.t, l, out=out[:, :, 0], **kw)
+    da.diffattn_fwd_decode_kv4(wide[:, 2:18, 1], c.t, l, out=out[:, :, 0], **kw)
     assert torch.equal(out[:, :, 0], base) and (out[:, :, 1] == 9.0).all()
-    for page in (2, 32, 512):
+    for page in (8, 32, 512):
         pc = Cache(2, 300, 2, page, seed=page).set_entries(rec)
         assert torch.equal(da.diffattn_fwd_decode_kv4(q, pc.t, l, **kw, **pc.where), base)
+    for other in (Cache(2, 300, 2, 2, seed=2), Cache(2, 300, 2, head_major=True),
+                  Cache(2, 300, 2, 16, seed=4, head_major=True)):
+        _check_decode(2, other.set_entries(rec), rec, q, qx, lam, lens)
+    # a pool whose records are further apart than they are long
+    apart = torch.full((2, 300, 2, 160), 0xFF, dtype=torch.uint8, device="cuda")
+    apart[..., :144] = c.t
+    c.t = apart[..., :144]
+    _check_decode(2, c, rec, q, qx, lam, lens)
+
+
+@pytest.mark.parametrize("H", [1, 2, 3, 4, 8])
+@pytest.mark.parametrize("page", [0, 2, 8, 128])
+def test_decode_ragged_batches(H, page):
+    """Many entries of very different lengths: blocks begin and end anywhere in the units."""
+    lens = [1, 700, 0, 0, 33, 64, 65, 2, 129, 700, 1, 1, 5, 300, 0]
+    case = _decode_case(2, len(lens), 4 * H, H, 700, lens, page, seed=H + page)
+    for splits in (0, 1, 2, 7):
+        _check_decode(2, *case, lens, num_splits=splits, what=f"splits {splits}")
+    lens = [0] * len(lens)
+    _check_decode(2, *case, lens)
 
 
 @pytest.mark.parametrize("variant", [1, 2])
@@ -476,8 +518,7 @@ def test_decode_is_deterministic_and_default_workspace_agrees():
     c, rec, q, qx, lam = _decode_case(2, 2, 16, 2, 3000, lens, seed=18)
     l, kl = torch.from_numpy(lam).cuda(), _i32(lens)
     base = da.diffattn_fwd_decode_kv4(q, c.t, l, kv_len=kl)
-    p, _ = da._binding.decode_kv4_params(q, c.t, None)
-    n = da.diffattn_decode_kv4_workspace_size(p)
+    n = da.diffattn_decode_kv4_workspace_size(*da._binding.decode_kv4_params(q, c.t, None))
     for fill in (0xFF, 0x00, 0x7F):  # the workspace's contents do not matter
         ws = torch.full((n,), fill, dtype=torch.uint8, device="cuda")
         assert torch.equal(da.diffattn_fwd_decode_kv4(q, c.t, l, kv_len=kl, workspace=ws), base)

@@ -142,16 +142,26 @@ def test_decode_pointers_norm_and_workspace(lib):
     assert _decode(lib, _params(), _pool()) == -1
     for kw, code in POOLS:
         assert _decode(lib, _params(), _pool(**kw), table=GOOD) == code
-    p = _params(num_splits=1, max_kv_len=1000, kv_strides=(1000 * 4 * REC, 4 * REC, REC))
+    # the workspace: two units' states of every block, 4 heads of 8 rows each here
     n = ctypes.c_size_t(1)
-    assert lib.diffattn_decode_kv4_workspace_size(ctypes.byref(p), ctypes.byref(n)) == 0 and n.value == 0
-    p.num_splits = 3
-    assert lib.diffattn_decode_kv4_workspace_size(ctypes.byref(p), ctypes.byref(n)) == 0
-    assert n.value == 2 * 16 * 3 * 130 * 4
+    size = lib.diffattn_decode_kv4_workspace_size
+    for splits, L, blocks in ((1, 1000, 2), (3, 1000, 6), (0, 1000, 32), (0, 64, 2), (9, 64, 4), (2, 0, 1)):
+        p = _params(num_splits=splits, max_kv_len=L, kv_strides=(1000 * 4 * REC, 4 * REC, REC))
+        assert size(ctypes.byref(p), None, ctypes.byref(n)) == 0
+        assert n.value == blocks * 2 * 4 * 8 * 130 * 4, (splits, L)
+    p = _params(max_kv_len=1 << 20, kv_strides=(4 * REC << 20, 4 * REC, REC), n_q_heads=64)
+    assert size(ctypes.byref(p), None, ctypes.byref(n)) == 0 and n.value < 20 << 20
+    # the pool's geometry takes part: pages under 8 tokens take one head to a block
+    assert size(ctypes.byref(_params()), ctypes.byref(_pool()), ctypes.byref(n)) == 0
+    assert n.value == 2 * 2 * 4 * 8 * 130 * 4
+    assert size(ctypes.byref(_params()), ctypes.byref(_pool(page_size=4, max_pages_per_seq=16)), ctypes.byref(n)) == 0
+    assert n.value == 4 * 2 * 1 * 8 * 130 * 4
+    p = _params()
+    assert size(ctypes.byref(p), None, ctypes.byref(n)) == 0
     assert _decode(lib, p, ws=None) == -4
     assert _decode(lib, p, ws_bytes=n.value - 1) == -4
     assert _decode(lib, p, ws=GOOD + 16) == -3
-    assert lib.diffattn_decode_kv4_workspace_size(ctypes.byref(p), None) == -1
+    assert size(ctypes.byref(p), None, None) == -1
     assert _decode(lib, _params(batch=0), q=None, cache=None, lam=None, out=None, ws=None) == 0
 
 
