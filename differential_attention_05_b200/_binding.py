@@ -651,25 +651,77 @@ def _kv4_cache(fn, cache, block_table, max_kv_len, batch):
     return pk, (0, 0, 0), L
 
 
-def _kv4_scope(device, stream):
-    """Make the cache's device and the launch stream current, so that allocations belong to
-    that stream and a call on tensors of another device than the current one lands there."""
-    import contextlib
+# What a call's checks and parameter structs come to, by the operands' shapes, strides, types
+# and devices (not their contents or addresses): a serving loop makes the same calls again and
+# again, and the checks cost more than the launch.
+_kv4_plans = {}
 
-    import torch
-    scope = contextlib.ExitStack()
-    if torch.cuda.current_device() != device.index:
-        scope.enter_context(torch.cuda.device(device))
-    if stream is not None:
-        if stream.device != device:
+
+def _kv4_plan(build, scalars, *tensors):
+    key = (build, scalars, *[None if t is None else (t.shape, t.stride(), t.dtype, t.device) for t in tensors])
+    plan = _kv4_plans.get(key)
+    if plan is None:
+        plan = build(scalars, *tensors)
+        if len(_kv4_plans) >= 4096:
+            _kv4_plans.clear()
+        _kv4_plans[key] = plan
+    return plan
+
+
+# the current stream's handle without a Stream object around it (6 us less a call), where this
+# torch has that
+try:
+    from torch._C import _cuda_getCurrentRawStream as _raw_stream
+except ImportError:  # pragma: no cover
+    _raw_stream = None
+
+
+class _Kv4Scope:
+    """Makes the cache's device and the launch stream current where they are not, so that
+    allocations belong to that stream and a call on tensors of another device than the current
+    one lands there. `raw` is the launch stream's handle."""
+
+    __slots__ = ("device", "stream", "raw", "stack")
+
+    def __init__(self, device, stream):
+        self.device, self.stream, self.stack = device, stream, None
+
+    def __enter__(self):
+        import torch
+        stream, device = self.stream, self.device
+        if stream is not None and stream.device != device:
             _kv4_fail("stream", f"the stream is on {stream.device}, the cache on {device}")
-        scope.enter_context(torch.cuda.stream(stream))
-    return scope
+        if stream is not None or torch.cuda.current_device() != device.index:
+            import contextlib
+            self.stack = contextlib.ExitStack()
+            self.stack.enter_context(torch.cuda.device(device))
+            if stream is not None:
+                self.stack.enter_context(torch.cuda.stream(stream))
+        if stream is not None:
+            self.raw = stream.cuda_stream
+        elif _raw_stream is not None:
+            self.raw = _raw_stream(device.index)
+        else:
+            self.raw = torch.cuda.current_stream(device).cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        if self.stack is not None:
+            self.stack.__exit__(*exc)
 
 
-def _kv4_rows(fn, k, v, cache, pos, cu_seqlens, max_seqlen, block_table, max_kv_len, dev_status):
-    """Parameter struct and pool geometry of a write or a read of rows k and v."""
+def _int(x):
+    return None if x is None else int(x)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _kv4_rows_plan(scalars, k, v, cache, pos, cu_seqlens, block_table, dev_status):
+    """(parameter struct, pool geometry or None) of a write or a read of rows k and v."""
     import torch
+    fn, max_seqlen, max_kv_len = scalars
     packed = cu_seqlens is not None
     lead = 1 if packed else 2
     for name, t in (("k", k), ("v", v)):
@@ -700,7 +752,7 @@ def _kv4_rows(fn, k, v, cache, pos, cu_seqlens, max_seqlen, block_table, max_kv_
     pk, p.cache_strides[:], p.max_kv_len = _kv4_cache(fn, cache, block_table, max_kv_len, p.batch)
     _kv4_tensor(fn, "pos", pos, torch.int32, cache.device, (p.batch,))
     _kv4_tensor(fn, "dev_status", dev_status, torch.int32, cache.device)
-    return p, None if pk is None else ctypes.byref(pk)
+    return ctypes.pointer(p), None if pk is None else ctypes.cast(ctypes.pointer(pk), ctypes.c_void_p), pk
 
 
 def diffattn_kv4_write(k, v, cache, pos=None, cu_seqlens=None, max_seqlen=None, block_table=None,
@@ -711,11 +763,11 @@ def diffattn_kv4_write(k, v, cache, pos=None, cu_seqlens=None, max_seqlen=None, 
     [B+1] and max_seqlen. cache uint8 [B,L,H,144], or a pool [P,page,H,144] with block_table.
     Returns cache."""
     lib = load_library()
-    p, pk = _kv4_rows("diffattn_kv4_write", k, v, cache, pos, cu_seqlens, max_seqlen, block_table,
-                      max_kv_len, dev_status)
-    with _kv4_scope(cache.device, stream):
-        rc = lib.diffattn_kv4_write(ctypes.byref(p), pk, _ptr(k), _ptr(v), _ptr(cu_seqlens), _ptr(pos),
-                                    _ptr(cache), _ptr(block_table), _ptr(dev_status), _stream(stream))
+    p, pk, _ = _kv4_plan(_kv4_rows_plan, ("diffattn_kv4_write", _int(max_seqlen), _int(max_kv_len)), k, v, cache, pos,
+                         cu_seqlens, block_table, dev_status)
+    with _Kv4Scope(cache.device, stream) as on:
+        rc = lib.diffattn_kv4_write(p, pk, k.data_ptr(), v.data_ptr(), _addr(cu_seqlens), _addr(pos),
+                                    cache.data_ptr(), _addr(block_table), _addr(dev_status), on.raw)
     _check("diffattn_kv4_write", rc)
     return cache
 
@@ -731,22 +783,24 @@ def diffattn_kv4_read(cache, n_tokens=None, pos=None, cu_seqlens=None, max_seqle
     lib = load_library()
     if (k is None) != (v is None):
         _kv4_fail("diffattn_kv4_read", "give both k and v or neither")
-    with _kv4_scope(cache.device, stream):
+    if not cache.is_cuda:
+        _kv4_fail("diffattn_kv4_read", "cache is not a CUDA tensor")
+    with _Kv4Scope(cache.device, stream) as on:
         if k is None:
             if n_tokens is None or cache.dim() != 4:
                 _kv4_fail("diffattn_kv4_read", "needs n_tokens or k and v, and a cache [., ., H, 144]")
             rows = (int(n_tokens),)
             if cu_seqlens is None:
-                rows = (int(cache.shape[0] if block_table is None else block_table.shape[0]), *rows)
+                rows = (cache.shape[0] if block_table is None else block_table.shape[0], rows[0])
             k = torch.empty((*rows, cache.shape[2], 128), dtype=dtype or torch.bfloat16, device=cache.device)
             v = torch.empty_like(k)
         elif (n_tokens is not None and int(n_tokens) != k.shape[0 if cu_seqlens is not None else 1]) or (
                 dtype is not None and dtype != k.dtype):
             _kv4_fail("diffattn_kv4_read", "n_tokens or dtype is not that of the given k")
-        p, pk = _kv4_rows("diffattn_kv4_read", k, v, cache, pos, cu_seqlens, max_seqlen, block_table,
-                          max_kv_len, dev_status)
-        rc = lib.diffattn_kv4_read(ctypes.byref(p), pk, _ptr(cache), _ptr(block_table), _ptr(cu_seqlens),
-                                   _ptr(pos), _ptr(k), _ptr(v), _ptr(dev_status), _stream(stream))
+        p, pk, _ = _kv4_plan(_kv4_rows_plan, ("diffattn_kv4_read", _int(max_seqlen), _int(max_kv_len)), k, v, cache, pos,
+                             cu_seqlens, block_table, dev_status)
+        rc = lib.diffattn_kv4_read(p, pk, cache.data_ptr(), _addr(block_table), _addr(cu_seqlens), _addr(pos),
+                                   k.data_ptr(), v.data_ptr(), _addr(dev_status), on.raw)
     _check("diffattn_kv4_read", rc)
     return k, v
 
@@ -781,19 +835,13 @@ def diffattn_decode_kv4_workspace_size(p: DecodeParams, pk=None) -> int:
     return int(n.value)
 
 
-def diffattn_fwd_decode_kv4(q, cache, lam, kv_len=None, lambda_init=None, out=None, apply_norm=None,
-                            norm_eps=1e-5, workspace=None, num_splits=0, block_table=None,
-                            max_kv_len=None, dev_status=None, stream=None):
-    """Split-KV differential decode over a 4-bit cache (see include/diffattn.h): uint8
-    [B,L,H,144], or a pool [P,page,H,144] with block_table int32 [B,pages]. V2: q [B,Hq,128] ->
-    out [B,Hq/2,128]. V1: q [B,H,2,64] -> out [B,H,128] (norm and scale when apply_norm, default
-    on). max_kv_len defaults to the positions the cache or the block table has room for."""
+def _kv4_decode_plan(scalars, q, cache, lam, kv_len, lambda_init, out, block_table, dev_status):
+    """(parameter struct, pool geometry or None, workspace bytes, output shape, V1)."""
     import torch
     fn = "diffattn_fwd_decode_kv4"
-    lib = load_library()
+    num_splits, max_kv_len = scalars
     p, pk = decode_kv4_params(q, cache, out, num_splits, block_table, max_kv_len)
     v1 = p.variant == DIFFATTN_V1
-    norm = v1 if apply_norm is None else bool(apply_norm)
     units = p.n_q_heads if v1 else p.n_q_heads // 2
     device = cache.device
     _kv4_tensor(fn, "q", q, torch.bfloat16, device, dense=False)
@@ -806,19 +854,37 @@ def diffattn_fwd_decode_kv4(q, cache, lam, kv_len=None, lambda_init=None, out=No
         if out.stride(-1) != 1:
             _kv4_fail(fn, "the channels of out must be contiguous")
     need = diffattn_decode_kv4_workspace_size(p, pk)
-    with _kv4_scope(device, stream):
+    return (ctypes.pointer(p), None if pk is None else ctypes.cast(ctypes.pointer(pk), ctypes.c_void_p), need,
+            (p.batch, units, 128), v1, pk)
+
+
+def diffattn_fwd_decode_kv4(q, cache, lam, kv_len=None, lambda_init=None, out=None, apply_norm=None,
+                            norm_eps=1e-5, workspace=None, num_splits=0, block_table=None,
+                            max_kv_len=None, dev_status=None, stream=None):
+    """Split-KV differential decode over a 4-bit cache (see include/diffattn.h): uint8
+    [B,L,H,144], or a pool [P,page,H,144] with block_table int32 [B,pages]. V2: q [B,Hq,128] ->
+    out [B,Hq/2,128]. V1: q [B,H,2,64] -> out [B,H,128] (norm and scale when apply_norm, default
+    on). max_kv_len defaults to the positions the cache or the block table has room for."""
+    import torch
+    lib = load_library()
+    p, pk, need, shape, v1, _ = _kv4_plan(_kv4_decode_plan, (int(num_splits), _int(max_kv_len)), q, cache, lam, kv_len,
+                                          lambda_init, out, block_table, dev_status)
+    device = cache.device
+    with _Kv4Scope(device, stream) as on:
         if out is None:
-            out = torch.empty((p.batch, units, 128), dtype=torch.bfloat16, device=device)
-        if workspace is None and need:
+            out = torch.empty(shape, dtype=torch.bfloat16, device=device)
+        if workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        if workspace is not None and (workspace.device != device or not workspace.is_contiguous()):
-            _kv4_fail(fn, "workspace must be contiguous and on the cache's device", -4)
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+            ws_bytes = need
+        else:
+            if workspace.device != device or not workspace.is_contiguous():
+                _kv4_fail("diffattn_fwd_decode_kv4", "workspace must be contiguous and on the cache's device", -4)
+            ws_bytes = workspace.numel() * workspace.element_size()
         rc = lib.diffattn_fwd_decode_kv4(
-            ctypes.byref(p), None if pk is None else ctypes.byref(pk), _ptr(q), _ptr(cache), _ptr(block_table),
-            _ptr(kv_len), _ptr(lam), _ptr(lambda_init), int(norm), float(norm_eps), _ptr(out), _ptr(workspace),
-            ws_bytes, _ptr(dev_status), _stream(stream))
-    _check(fn, rc)
+            p, pk, q.data_ptr(), cache.data_ptr(), _addr(block_table), _addr(kv_len), lam.data_ptr(),
+            _addr(lambda_init), int(v1 if apply_norm is None else bool(apply_norm)), norm_eps, out.data_ptr(),
+            workspace.data_ptr(), ws_bytes, _addr(dev_status), on.raw)
+    _check("diffattn_fwd_decode_kv4", rc)
     return out
 
 

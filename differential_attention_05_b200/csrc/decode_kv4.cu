@@ -899,15 +899,24 @@ static cudaError_t launch_split(const DecodeKv4Args& a, cudaStream_t stream) {
   const int page = 1 << a.cache.page_shift;
   CUtensorMap map;
   memset(&map, 0, sizeof(map));
-  void (*fn)(CUtensorMap, DecodeKv4Args) = decode_kv4_split_kernel<NT, HB, kCopy>;
-  if (!paged && kv4_map<HB>(&map, a.cache, a.H, a.cache.L, a.B, TL::CK)) {
-    fn = decode_kv4_split_kernel<NT, HB, kTma>;
-  } else if (paged && page >= 8 &&
-             kv4_map<HB>(&map, a.cache, a.H, page, a.cache.num_pages, page < TL::CK ? page : TL::CK)) {
-    fn = decode_kv4_split_kernel<NT, HB, kTmaPaged>;
-  }
-  cudaError_t e = cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, TL::SMEM_BYTES);
+  Kv4Load how = kCopy;
+  if (!paged && kv4_map<HB>(&map, a.cache, a.H, a.cache.L, a.B, TL::CK)) how = kTma;
+  if (paged && page >= 8 &&
+      kv4_map<HB>(&map, a.cache, a.H, page, a.cache.num_pages, page < TL::CK ? page : TL::CK))
+    how = kTmaPaged;
+  void (*const fns[3])(CUtensorMap, DecodeKv4Args) = {decode_kv4_split_kernel<NT, HB, kTma>,
+                                                      decode_kv4_split_kernel<NT, HB, kTmaPaged>,
+                                                      decode_kv4_split_kernel<NT, HB, kCopy>};
+  void (*const fn)(CUtensorMap, DecodeKv4Args) = fns[how];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  static bool attr_set[3][64] = {};
+  if (dev >= 64 || !attr_set[how][dev]) {
+    e = cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, TL::SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) attr_set[how][dev] = true;
+  }
   fn<<<(unsigned)a.blocks, THREADS, TL::SMEM_BYTES, stream>>>(map, a);
   return cudaGetLastError();
 }
