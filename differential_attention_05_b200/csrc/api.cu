@@ -630,7 +630,7 @@ static int kv4_rows_run(bool write, const diffattn_kv4_rows* p, const diffattn_p
   if (p->batch < 0 || p->n_tokens < 0 || per < 0 || p->n_kv_heads < 1 || p->max_kv_len < 0)
     return DIFFATTN_ERR_INVALID_ARG;
   if (p->batch > 65535 || p->n_kv_heads > 65535 || p->max_kv_len > (1 << 30)) return DIFFATTN_ERR_UNSUPPORTED;
-  if ((int64_t)per * p->n_kv_heads > (int64_t)1 << 35) return DIFFATTN_ERR_UNSUPPORTED;  // the launch's grid
+  if ((int64_t)per * p->n_kv_heads > INT32_MAX) return DIFFATTN_ERR_UNSUPPORTED;  // 32-bit record numbers
   if (!strides_ok(p->k_strides, 3) || !strides_ok(p->v_strides, 3)) return DIFFATTN_ERR_INVALID_ARG;
   Kv4RowsArgs a;
   memset(&a, 0, sizeof(a));

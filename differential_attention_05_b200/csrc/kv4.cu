@@ -4,24 +4,30 @@
 // (the negative one where +|x*| and -|x*| both occur),
 //   scale = -x* / 8,   n_i = clamp(round(x_i / scale), -8, 7) + 8,
 // round to nearest, ties to even. Dividing a bf16 value by 8 is exact, so x* itself is held
-// exactly (code -8), and x_i / scale is a quotient of two 8-bit significands: it is a tie or
-// at least 2^-9 away from one in relative terms, so the rounded fp32 division decides every
-// code as exact arithmetic would. Groups with |x*| < 2^-100 are held as zeros (their scale
+// exactly (code -8). Groups with |x*| < 2^-100 are held as zeros (their scale
 // would near the subnormals); a group with a NaN or an infinity gets a NaN scale, so that
 // its values read back as NaN.
 //
-// Both kernels move bytes: one warp takes one (token, head) at a time, lanes 0..15 its K
-// row, lanes 16..31 its V row, 8 channels (4 code bytes) each, so the codes of a record are
-// one 128-byte run of a warp's 4-byte accesses and four lanes share a scale. A warp holds
-// RECS records in flight, because one 16-byte load per lane does not cover the latency.
+// The kernels write n without a division for each element: with r = 1 / scale rounded,
+// x r is within 2^-22 of x / scale in relative terms, and adding and taking away 1.5 * 2^11
+// rounds it to a multiple of 2^-12; a tie comes out exactly, and anything else stays on its
+// side of one (x / scale is at most 8 in magnitude and at least 2^-10 from a tie it does not
+// meet, having two 8-bit significands). A second such constant then rounds to an integer.
+//
+// Both kernels move bytes, and at first their index arithmetic cost more than the work on the
+// channels (164 instructions a record, 107 us for 65536 tokens x 8 heads, with a warp to a
+// record). Now a half-warp takes a record: lanes 0..7 its K row, 8..15 its V row, each lane
+// channels 8 c .. 8 c + 7 and 64 more of them further on, so the rows are runs of 128 bytes
+// and four lanes share a scale. A warp takes 2 STEPS records, neighbouring heads first and
+// then the next tokens, with the loads of all in flight together.
 #include "kv4.cuh"
 
 namespace diffattn {
 
 namespace {
 constexpr int WARPS = 8;
-constexpr int RECS = 4;                 // records of a warp in flight
-constexpr int PER_BLOCK = WARPS * RECS;
+constexpr int kSteps = 4;     // pairs of records of a warp (bf16 rows)
+constexpr int kStepsF32 = 2;  // and of fp32 rows, twice as wide
 }  // namespace
 
 // The rows of entry b: their count and the first one's row in packed tensors. Offsets that
@@ -43,177 +49,228 @@ __device__ __forceinline__ Kv4Entry kv4_entry(const Kv4RowsArgs& a, int b) {
   return e;
 }
 
-// Element offset of this lane's 8 channels in the K or V tensor, for row i of entry b.
-__device__ __forceinline__ int64_t kv4_row_offset(const Kv4RowsArgs& a, const Kv4Entry& e, int b, int i,
-                                                  int h, int lane) {
-  const int64_t* s = lane < 16 ? a.ks : a.vs;
-  return (a.cu ? (int64_t)(e.row0 + i) * s[1] : b * s[0] + i * s[1]) + h * s[2] + (lane & 15) * 8;
+// Where this lane's channels are: of record r of the warp's, in the K or V tensor (elements)
+// and in the cache (bytes; -1: its position or page is outside).
+struct Kv4Lane {
+  const Kv4RowsArgs& a;
+  int b, n, i0, h0, c, v;
+  int64_t pos, base, s1, s2;
+  __device__ __forceinline__ Kv4Lane(const Kv4RowsArgs& args, const Kv4Entry& e, int entry, int lane, int recs)
+      : a(args), b(entry), n(e.n) {
+    const uint32_t item = blockIdx.x * WARPS + (threadIdx.x >> 5);
+    const uint32_t head_items = (uint32_t)a.H >> a.head_shift;
+    const uint32_t row_item = item / head_items;
+    i0 = (int)(row_item * (uint32_t)(recs >> a.head_shift));
+    h0 = (int)(item - row_item * head_items) << a.head_shift;
+    c = lane & 7;
+    v = (lane >> 3) & 1;
+    pos = a.pos ? __ldg(a.pos + b) : 0;
+    s1 = v ? a.vs[1] : a.ks[1];
+    s2 = v ? a.vs[2] : a.ks[2];
+    base = (a.cu ? e.row0 * s1 : b * (v ? a.vs[0] : a.ks[0])) + c * 8;
+  }
+  __device__ __forceinline__ int row(int r) const { return i0 + (r >> a.head_shift); }
+  __device__ __forceinline__ int head(int r) const { return h0 + (r & ((1 << a.head_shift) - 1)); }
+  __device__ __forceinline__ int64_t channels(int r) const { return base + row(r) * s1 + head(r) * s2; }
+  __device__ __forceinline__ int64_t record(int r) const {
+    const int64_t t = pos + row(r);
+    if (t < 0 || t >= a.cache.L) return -1;
+    const int64_t at = kv4_page_offset(a.cache, b, (int)t);
+    return at < 0 ? -1 : at + head(r) * a.cache.stride[2];
+  }
+};
+
+// 8 codes and the bf16 bits of the scale of 8 channels (bf16 pairs w), which with those of
+// the three lanes beside it make a group
+__device__ __forceinline__ uint32_t kv4_encode(const uint32_t (&w)[4], uint32_t& scale_bits) {
+  // The largest magnitude among the group's positive values (low half) and among its
+  // negative ones (high half), on bf16 bits: as signed 16-bit integers the largest is the
+  // largest positive value, as unsigned ones the largest negative one.
+  const uint32_t up = __vmaxs2(__vmaxs2(w[0], w[1]), __vmaxs2(w[2], w[3]));
+  const uint32_t down = __vmaxu2(__vmaxu2(w[0], w[1]), __vmaxu2(w[2], w[3]));
+  const int pos = max(max((int)(int16_t)up, (int)up >> 16), 0);
+  const int neg = max((int)max(down & 0xffffu, down >> 16) - 0x8000, 0);
+  uint32_t most = (uint32_t)pos | (uint32_t)neg << 16;
+  most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, 1));
+  most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, 2));
+  const uint32_t p16 = most & 0xffffu, n16 = most >> 16, size = max(p16, n16);
+  const bool finite = size < 0x7f80u;
+  const bool held = finite && size >= (27u << 7);  // not under 2^-100
+  const float peak = __uint_as_float(size << 16);
+  const float scale = n16 >= p16 ? peak * 0.125f : peak * -0.125f;
+  // kFine in [2^11, 2^12): units of 2^-12; adding kWhole - kFine, exact up to its own
+  // rounding, then gives the integer on top of kWhole = 1.5 * 2^23
+  constexpr float kFine = 1.5f * 2048.f, kWhole = 12582912.f;
+  const float inv = __frcp_rn(scale);
+  float2 k[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float2 t = fma2(make_float2(bf16_low(w[i]), bf16_high(w[i])), make_float2(inv, inv), make_float2(kFine, kFine));
+    t = make_float2(fminf(t.x, kFine + 7.f), fminf(t.y, kFine + 7.f));
+    k[i] = add2(add2(t, make_float2(kWhole - kFine, kWhole - kFine)), make_float2(-kWhole, -kWhole));
+  }
+  // four codes as the digits of a number, 8 added to each, in the low 16 bits of a float
+  const float2 even = fma2(k[1], make_float2(256.f, 256.f), k[0]), odd = fma2(k[3], make_float2(256.f, 256.f), k[2]);
+  const float lo = __fmaf_rn(even.y, 16.f, even.x) + (kWhole + 34952.f);  // 0x8888
+  const float hi = __fmaf_rn(odd.y, 16.f, odd.x) + (kWhole + 34952.f);
+  scale_bits = !finite ? 0x7fc0u : (held ? __float_as_uint(scale) >> 16 : 0u);
+  return held ? __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x5410) : 0x88888888u;
 }
 
 template <bool F32>
 __global__ void __launch_bounds__(WARPS * 32) kv4_write_kernel(Kv4RowsArgs a) {
-  const int b = blockIdx.y, lane = threadIdx.x & 31;
+  constexpr int STEPS = F32 ? kStepsF32 : kSteps;
+  const int b = blockIdx.y, lane = threadIdx.x & 31, sub = lane >> 4;
   const Kv4Entry e = kv4_entry(a, b);
   if (!e.ok) {
     if (blockIdx.x == 0 && threadIdx.x == 0) report_status(a.cache.dev_status, DIFFATTN_ERR_INVALID_ARG);
     return;
   }
-  const int64_t recs = (int64_t)e.n * a.H;
-  const int64_t r0 = ((int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5)) * RECS;
-  if (r0 >= recs) return;
-  const int64_t pos = a.pos ? __ldg(a.pos + b) : 0;
-  const int64_t ext = lane < 16 ? a.ext_k : a.ext_v;
-  const void* src = lane < 16 ? a.k : a.v;
+  const Kv4Lane at(a, e, b, lane, 2 * STEPS);
+  if (at.i0 >= e.n) return;
+  const int64_t ext = at.v ? a.ext_v : a.ext_k;
+  const void* src = at.v ? a.v : a.k;
 
-  uint32_t raw[RECS][4];  // 8 channels of each record in bf16
-  int64_t dst[RECS];      // byte offset of the record, -1: not written
+  uint32_t raw[F32 ? 1 : STEPS][2][4];  // 8 channels and the 8 at 64 further on
+  float4 wide[F32 ? STEPS : 1][2][2];
+  int64_t dst[STEPS];  // byte offset of the record, -1: not written
 #pragma unroll
-  for (int r = 0; r < RECS; ++r) {
-    dst[r] = -1;
-    if (r0 + r >= recs) continue;
-    const int i = (int)((r0 + r) / a.H), h = (int)((r0 + r) - (int64_t)i * a.H);
-    const int64_t t = pos + i;
-    if (t >= 0 && t < a.cache.L) dst[r] = kv4_page_offset(a.cache, b, (int)t);
-    if (dst[r] >= 0) {
-      dst[r] += h * a.cache.stride[2];
-      if (!in_bounds(dst[r], kKv4Record, a.cache.ext, a.cache.dev_status, a.cache.dbg_status)) dst[r] = -1;
-    } else if (lane == 0) {
-      report_status(a.cache.dev_status, DIFFATTN_ERR_INVALID_ARG);
-    }
-    const int64_t off = kv4_row_offset(a, e, b, i, h, lane);
-    const bool ok = in_bounds(off, 8, ext, a.cache.dev_status, a.cache.dbg_status);
-    if (F32) {
-      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(src) + off);
-      const float4 x = ok ? p[0] : make_float4(0.f, 0.f, 0.f, 0.f);
-      const float4 y = ok ? p[1] : make_float4(0.f, 0.f, 0.f, 0.f);
-      raw[r][0] = pack_bf16(x.x, x.y); raw[r][1] = pack_bf16(x.z, x.w);
-      raw[r][2] = pack_bf16(y.x, y.y); raw[r][3] = pack_bf16(y.z, y.w);
-    } else {
-      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(src) + off);
-      const uint4 x = ok ? *p : make_uint4(0u, 0u, 0u, 0u);
-      raw[r][0] = x.x; raw[r][1] = x.y; raw[r][2] = x.z; raw[r][3] = x.w;
-    }
-  }
+  for (int s = 0; s < STEPS; ++s) {
+    const int r = 2 * s + sub;
+    const bool mine = at.row(r) < e.n;
+    dst[s] = mine ? at.record(r) : -1;
+    const int64_t off = at.channels(r);
 #pragma unroll
-  for (int r = 0; r < RECS; ++r) {
-    if (r0 + r >= recs) break;
-    float x[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = bf16_low(raw[r][i]);
-      x[2 * i + 1] = bf16_high(raw[r][i]);
-    }
-    // the group's largest and smallest value and whether all are finite, over its 4 lanes
-    float hi = x[0], lo = x[0];
-    bool finite = true;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      hi = fmaxf(hi, x[i]);
-      lo = fminf(lo, x[i]);
-      finite = finite && (__float_as_uint(x[i]) & 0x7f800000u) != 0x7f800000u;
-    }
-#pragma unroll
-    for (int o = 1; o <= 2; o <<= 1) {
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-      finite = __shfl_xor_sync(0xffffffffu, (int)finite, o) && finite;
-    }
-    const float peak = hi > -lo ? hi : lo;
-    const bool zero = fabsf(peak) < 7.888609052210118e-31f;  // 2^-100
-    const float scale = peak * -0.125f;
-    uint32_t codes = 0x88888888u;
-    if (finite && !zero) {
-      codes = 0u;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float n = fminf(fmaxf(rintf(__fdiv_rn(x[i], scale)), -8.f), 7.f);
-        codes |= (uint32_t)((int)n + 8) << (4 * i);
+    for (int q = 0; q < 2; ++q) {
+      const bool ok = mine && in_bounds(off + 64 * q, 8, ext, a.cache.dev_status, a.cache.dbg_status);
+      if constexpr (F32) {
+        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(src) + off + 64 * q);
+        wide[s][q][0] = ok ? __ldcs(p) : make_float4(0.f, 0.f, 0.f, 0.f);
+        wide[s][q][1] = ok ? __ldcs(p + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+      } else {
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(src) + off + 64 * q);
+        const uint4 x = ok ? __ldcs(p) : make_uint4(0u, 0u, 0u, 0u);
+        raw[s][q][0] = x.x; raw[s][q][1] = x.y; raw[s][q][2] = x.z; raw[s][q][3] = x.w;
       }
     }
-    // bf16 bits of the scale (exact: a power of two times a bf16 value)
-    const uint32_t sb = !finite ? 0x7fc0u : (zero ? 0u : __float_as_uint(scale) >> 16);
-    const uint32_t pair = sb | (__shfl_down_sync(0xffffffffu, sb, 4) << 16);
-    if (dst[r] >= 0) {
-      uint8_t* rec = a.cache.base + dst[r];
-      reinterpret_cast<uint32_t*>(rec)[lane] = codes;
-      if ((lane & 7) == 0) reinterpret_cast<uint32_t*>(rec + kKv4Scales)[lane >> 3] = pair;
+    if (mine && dst[s] < 0 && (lane & 15) == 0) report_status(a.cache.dev_status, DIFFATTN_ERR_INVALID_ARG);
+    if (dst[s] >= 0 && !in_bounds(dst[s], kKv4Record, a.cache.ext, a.cache.dev_status, a.cache.dbg_status)) dst[s] = -1;
+  }
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    uint32_t codes[2], bits[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      if constexpr (F32) {
+        const float4 x = wide[s][q][0], y = wide[s][q][1];
+        const uint32_t w[4] = {pack_bf16(x.x, x.y), pack_bf16(x.z, x.w), pack_bf16(y.x, y.y), pack_bf16(y.z, y.w)};
+        codes[q] = kv4_encode(w, bits[q]);
+      } else {
+        codes[q] = kv4_encode(raw[s][q], bits[q]);
+      }
+      bits[q] |= __shfl_down_sync(0xffffffffu, bits[q], 4) << 16;  // lane c = 0: groups 2 q, 2 q + 1
+    }
+    if (dst[s] >= 0) {
+      uint32_t* row = reinterpret_cast<uint32_t*>(a.cache.base + dst[s]) + at.v * 16 + at.c;
+      row[0] = codes[0];
+      row[8] = codes[1];
+      if (at.c == 0)
+        *reinterpret_cast<uint2*>(a.cache.base + dst[s] + kKv4Scales + at.v * 8) = make_uint2(bits[0], bits[1]);
     }
   }
 }
 
-// Reading back: each lane turns 4 code bytes and its group's scale into 8 channels,
-// scale * (n - 8): 12 significant bits, exact in fp32 and rounded once to bf16 (nearest).
+// Channels 2 i and 2 i + 1 of a word of 8 codes, as two bf16 values n - 8 (exact: 128 + n - 136)
+template <int I>
+__device__ __forceinline__ __nv_bfloat162 kv4_pair(uint32_t w) {
+  const uint32_t lo = w >> (8 * I), hi = I < 2 ? w << (12 - 8 * I) : w >> (8 * I - 12);
+  const uint32_t x = (lo & 0xfu) | (hi & 0xf0000u) | 0x43004300u;
+  return __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), __float2bfloat162_rn(136.f));
+}
+
+// Reading back: each lane turns 4 code bytes and their group's scale into 8 channels, twice:
+// scale * (n - 8) has 12 significant bits, exact in fp32 and rounded once to bf16 (nearest).
 template <bool F32>
 __global__ void __launch_bounds__(WARPS * 32) kv4_read_kernel(Kv4RowsArgs a) {
-  const int b = blockIdx.y, lane = threadIdx.x & 31;
+  constexpr int STEPS = F32 ? kStepsF32 : kSteps;
+  const int b = blockIdx.y, lane = threadIdx.x & 31, sub = lane >> 4;
   const Kv4Entry e = kv4_entry(a, b);
   if (!e.ok) {
     if (blockIdx.x == 0 && threadIdx.x == 0) report_status(a.cache.dev_status, DIFFATTN_ERR_INVALID_ARG);
     return;
   }
-  const int64_t recs = (int64_t)e.n * a.H;
-  const int64_t r0 = ((int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5)) * RECS;
-  if (r0 >= recs) return;
-  const int64_t pos = a.pos ? __ldg(a.pos + b) : 0;
-  const int64_t ext = lane < 16 ? a.ext_k : a.ext_v;
-  void* dst = lane < 16 ? a.k : a.v;
+  const Kv4Lane at(a, e, b, lane, 2 * STEPS);
+  if (at.i0 >= e.n) return;
+  const int64_t ext = at.v ? a.ext_v : a.ext_k;
+  void* dst = at.v ? a.v : a.k;
 
-  uint32_t codes[RECS];
-  float scale[RECS];
-  int64_t off[RECS];  // element offset of this lane's 8 channels
+  uint32_t codes[STEPS][2], scale[STEPS][2];  // scale: bf16 bits
 #pragma unroll
-  for (int r = 0; r < RECS; ++r) {
-    codes[r] = 0u;
-    scale[r] = 0.f;
-    off[r] = -1;
-    if (r0 + r >= recs) continue;
-    const int i = (int)((r0 + r) / a.H), h = (int)((r0 + r) - (int64_t)i * a.H);
-    off[r] = kv4_row_offset(a, e, b, i, h, lane);
-    const int64_t t = pos + i;
-    int64_t at = -1;
-    if (t >= 0 && t < a.cache.L) at = kv4_page_offset(a.cache, b, (int)t);
-    if (at < 0) {  // outside the entry or the pool: the row reads as zeros
-      if (lane == 0) report_status(a.cache.dev_status, DIFFATTN_ERR_INVALID_ARG);
-      continue;
+  for (int s = 0; s < STEPS; ++s) {
+    const int r = 2 * s + sub;
+    const bool mine = at.row(r) < e.n;
+    const int64_t from = mine ? at.record(r) : -1;
+    // outside the entry or the pool: the row reads as zeros
+    if (mine && from < 0 && (lane & 15) == 0) report_status(a.cache.dev_status, DIFFATTN_ERR_INVALID_ARG);
+    const bool ok = from >= 0 && in_bounds(from, kKv4Record, a.cache.ext, a.cache.dev_status, a.cache.dbg_status);
+    const uint8_t* rec = a.cache.base + (ok ? from : 0);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      codes[s][q] = ok ? __ldcs(reinterpret_cast<const uint32_t*>(rec) + at.v * 16 + 8 * q + at.c) : 0u;
+      scale[s][q] = ok ? __ldcs(reinterpret_cast<const uint16_t*>(rec + kKv4Scales) + at.v * 4 + 2 * q + (at.c >> 2)) : 0u;
     }
-    at += h * a.cache.stride[2];
-    if (!in_bounds(at, kKv4Record, a.cache.ext, a.cache.dev_status, a.cache.dbg_status)) continue;
-    const uint8_t* rec = a.cache.base + at;
-    codes[r] = reinterpret_cast<const uint32_t*>(rec)[lane];
-    scale[r] = __uint_as_float(
-        (uint32_t)reinterpret_cast<const uint16_t*>(rec + kKv4Scales)[lane >> 2] << 16);
   }
 #pragma unroll
-  for (int r = 0; r < RECS; ++r) {
-    if (off[r] < 0 || !in_bounds(off[r], 8, ext, a.cache.dev_status, a.cache.dbg_status)) continue;
-    float x[8];
+  for (int s = 0; s < STEPS; ++s) {
+    const int r = 2 * s + sub;
+    if (at.row(r) >= e.n) break;
+    const int64_t off = at.channels(r);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = scale[r] * (float)((int)((codes[r] >> (4 * i)) & 15u) - 8);
-    if (F32) {
-      float4* p = reinterpret_cast<float4*>(static_cast<float*>(dst) + off[r]);
-      p[0] = make_float4(x[0], x[1], x[2], x[3]);
-      p[1] = make_float4(x[4], x[5], x[6], x[7]);
-    } else {
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(dst) + off[r]) =
-          make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+    for (int q = 0; q < 2; ++q) {
+      if (!in_bounds(off + 64 * q, 8, ext, a.cache.dev_status, a.cache.dbg_status)) continue;
+      const uint32_t w = codes[s][q];
+      const __nv_bfloat162 n[4] = {kv4_pair<0>(w), kv4_pair<1>(w), kv4_pair<2>(w), kv4_pair<3>(w)};
+      if constexpr (F32) {
+        const float f = __uint_as_float(scale[s][q] << 16);
+        float4* p = reinterpret_cast<float4*>(static_cast<float*>(dst) + off + 64 * q);
+        const float2 x0 = __bfloat1622float2(n[0]), x1 = __bfloat1622float2(n[1]);
+        const float2 x2 = __bfloat1622float2(n[2]), x3 = __bfloat1622float2(n[3]);
+        __stcs(p, make_float4(f * x0.x, f * x0.y, f * x1.x, f * x1.y));
+        __stcs(p + 1, make_float4(f * x2.x, f * x2.y, f * x3.x, f * x3.y));
+      } else {
+        const uint32_t both = scale[s][q] | scale[s][q] << 16;
+        const __nv_bfloat162 f = *reinterpret_cast<const __nv_bfloat162*>(&both);
+        uint32_t y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __nv_bfloat162 x = __hmul2(n[i], f);
+          y[i] = *reinterpret_cast<const uint32_t*>(&x);
+        }
+        __stcs(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(dst) + off + 64 * q),
+               make_uint4(y[0], y[1], y[2], y[3]));
+      }
     }
   }
 }
 
-static dim3 kv4_grid(const Kv4RowsArgs& a) {
-  return dim3((unsigned)(((int64_t)a.N * a.H + PER_BLOCK - 1) / PER_BLOCK), (unsigned)a.B);
+// A warp's records: 2^head_shift neighbouring heads (as many of its 2 STEPS as divide H) by rows.
+static cudaError_t kv4_launch(Kv4RowsArgs a, void (*fn)(Kv4RowsArgs), int recs, cudaStream_t stream) {
+  a.head_shift = 0;
+  while ((2 << a.head_shift) <= recs && a.H % (2 << a.head_shift) == 0) ++a.head_shift;
+  const int64_t rows = recs >> a.head_shift;
+  const int64_t items = ((int64_t)a.N + rows - 1) / rows * (a.H >> a.head_shift);
+  fn<<<dim3((unsigned)((items + WARPS - 1) / WARPS), (unsigned)a.B), WARPS * 32, 0, stream>>>(a);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_kv4_write(const Kv4RowsArgs& a, cudaStream_t stream) {
-  if (a.f32) kv4_write_kernel<true><<<kv4_grid(a), WARPS * 32, 0, stream>>>(a);
-  else kv4_write_kernel<false><<<kv4_grid(a), WARPS * 32, 0, stream>>>(a);
-  return cudaGetLastError();
+  return a.f32 ? kv4_launch(a, kv4_write_kernel<true>, 2 * kStepsF32, stream)
+               : kv4_launch(a, kv4_write_kernel<false>, 2 * kSteps, stream);
 }
 
 cudaError_t launch_kv4_read(const Kv4RowsArgs& a, cudaStream_t stream) {
-  if (a.f32) kv4_read_kernel<true><<<kv4_grid(a), WARPS * 32, 0, stream>>>(a);
-  else kv4_read_kernel<false><<<kv4_grid(a), WARPS * 32, 0, stream>>>(a);
-  return cudaGetLastError();
+  return a.f32 ? kv4_launch(a, kv4_read_kernel<true>, 2 * kStepsF32, stream)
+               : kv4_launch(a, kv4_read_kernel<false>, 2 * kSteps, stream);
 }
 
 }  // namespace diffattn
