@@ -8,18 +8,18 @@
 // Concept). V1 is the same with two rows for each head: branch 1 is (q_1 | 0) and branch 2
 // (0 | q_2) over the cached row (K_1 | K_2), and the norm and scale follow.
 //
-// One block takes (batch entry, KV head, split of the keys, up to 8 NT query rows). Its four
-// warps work alone, each on 32 keys of every 128: a ring of cp.async stages of its own, its
-// own running maximum, sums and output; the block joins them at the end, a second kernel
-// joins the splits. Products run on mma.sync m16n8k16 in fp16 with fp32 sums, keys (or value
+// A block takes up to four neighbouring KV heads and a run of tokens; one warp issues the
+// copies into a ring of stages, the others compute, each with 32 keys of a head at a time and
+// its own running maximum, sums and output; a second kernel joins what several blocks did of
+// an entry. Products run on mma.sync m16n8k16 in fp16 with fp32 sums, keys (or value
 // channels) as the 16 rows and query rows as the 8 columns:
 //   * Codes go from shared memory to registers by ldmatrix (keys: one 16-byte group of a row
 //     per matrix row, a thread gets 8 channels of one key; values: transposed, a thread gets
 //     4 channels of two neighbouring keys, which is the pair an MMA operand register holds).
 //   * K nibbles are used as fp16 subnormals: n in the low mantissa bits is n 2^-24, the next
-//     nibble 16 n 2^-24 against q / 16, so unpacking is one AND for two channels. The -8 is
-//     the accumulators' start, -8 * 2^-24 sum q: exact up to the fp32 sums, since half the
-//     range is all that cancels.
+//     nibble 16 n 2^-24 against q / 16, so unpacking is one AND for two channels. The -8 comes
+//     in as a product of the scales and -8 * 2^-24 sum q (in three bf16 parts), one MMA for 16
+//     keys, from which the scores start: half the range is all that cancels.
 //   * V nibbles become n - 8 exactly (0x6400 | n is 1024 + n). Left as subnormals with the -8
 //     from a second MMA over constants the full step took 455 us instead of 469, but the
 //     cancelling sums lost up to 2^-16 of a scale, which shows where a peaked row's key has
@@ -44,32 +44,41 @@ namespace diffattn {
 
 namespace {
 constexpr int W = kKv4Width;
-constexpr int WARPS = 4;
-constexpr int THREADS = WARPS * 32;
 constexpr int KEYS = 32;      // keys that a warp takes of a chunk
-constexpr float kTop = 8.f;   // p * scale <= 2^kTop when M is raised ...
+constexpr float kTop = 8.f;   // p * scale <= 2^kTop when the maximum is raised ...
 constexpr float kSlack = 7.f; // ... and <= 2^(kTop + kSlack) before
-static_assert(W == THREADS, "one thread per value channel in the joins");
 
-// A block takes HB neighbouring KV heads, WARPS / HB warps for each. A chunk is CK tokens in
-// a stage of one row per token: the HB records side by side, as they lie in the cache, and 16
+// A block has CW warps that compute and one that issues the copies: with NT = 1 (up to 8 query
+// rows) 4 of them, three blocks to an SM; with NT = 2 the accumulators of 16 rows need twice
+// the registers, and one block of 8 has an SM to itself.
+constexpr int compute_warps(int nt) { return nt == 1 ? 4 : 8; }
+
+// A block takes HB neighbouring KV heads, CW / HB warps for each. A chunk is CK tokens in a
+// stage of one row per token: the HB records side by side, as they lie in the cache, and 16
 // bytes more (of the next record, unused) where that is needed for a pitch that is an odd
 // number of 16-byte units, so that ldmatrix's 8 rows meet no bank twice.
-template <int HB>
+template <int NT, int HB>
 struct Tile {
-  static constexpr int PER_HEAD = WARPS / HB;  // warps of a head
+  static constexpr int CW = compute_warps(NT);
+  static constexpr int THREADS = (CW + 1) * 32;
+  static constexpr int BLOCKS_PER_SM = NT == 1 ? 3 : 1;
+  static constexpr int PER_HEAD = CW / HB;  // warps of a head
   static constexpr int CK = KEYS * PER_HEAD;
   static constexpr int PITCH = HB * kKv4Record + (HB == 1 ? 0 : 16);
-  static constexpr int STAGES = HB == 2 ? 3 : 4;  // what shared memory holds for three blocks
   static constexpr int STAGE_BYTES = CK * PITCH;
-  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES;
+  // what shared memory holds beside the states that the warps of a head join at the end
+  static constexpr int STAGES = NT == 1 ? (HB == 4 ? 4 : 3) : (HB == 4 ? 5 : 4);
+  static constexpr int ROWS = 8 * NT;
+  static constexpr int JOIN_FLOATS = (PER_HEAD - 1) * HB * ROWS * (W + 2);
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + JOIN_FLOATS * 4;
   static_assert((PITCH / 16) % 2 == 1 && STAGE_BYTES % 128 == 0 && 8 * PITCH % 128 == 0, "layout");
+  static_assert(BLOCKS_PER_SM * (SMEM_BYTES + 2048) <= 228 * 1024 && SMEM_BYTES <= 227 * 1024, "shared memory");
 };
 
 // How a chunk reaches shared memory: TMA boxes of CK rows (contiguous) or of a page's run of
 // up to CK (pages of 8 tokens and more; a box of fewer would not end on a 128-byte boundary),
-// or 16-byte copies (smaller pages, and strides that TMA does not take).
-enum Kv4Load { kTma, kTmaPaged, kCopy };
+// or one bulk copy for each token (smaller pages, and strides that TMA does not take).
+enum Kv4Load { kTma, kTmaPaged, kRows };
 }  // namespace
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -80,7 +89,7 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
-// d = a b + c
+// d = a b + c; mma_f16 without c and mma_bf16: d = a b
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1, const float (&c)[4]) {
   asm volatile(
@@ -88,6 +97,22 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       "{%8,%9}, {%10,%11,%12,%13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 // the even and the odd nibbles of the low byte of each half of w, as fp16: n 2^-24, 16 n 2^-24
 __device__ __forceinline__ uint32_t nib_even(uint32_t w) { return w & 0x000f000fu; }
@@ -122,28 +147,15 @@ __device__ __forceinline__ uint32_t code_odd(uint32_t w, const Magic& k) {
   const __half2 y = __hfma2(and_or(w, k.odd, k.magic), __float2half2_rn(0.0625f), __float2half2_rn(-72.f));
   return *reinterpret_cast<const uint32_t*>(&y);
 }
+// a load that stays where it is written
+__device__ __forceinline__ uint2 lds_uint2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-// The output of one unit (V1 head or V2 pair) from its branches' attention outputs, channel
-// `c` of the W threads with `mine`: the difference, and V1's norm and scale. All threads of the
-// block take part; `red` holds 4 floats.
-__device__ __forceinline__ void store_unit(const DecodeKv4Args& a, int b, int u, int c, bool mine, float o1,
-                                           float o2, float* red) {
-  float y = o1 - __ldg(a.lambda + u) * o2;
-  if (a.apply_norm) {
-    const float ss = warp_sum(y * y);
-    if (mine && (c & 31) == 0) red[c >> 5] = ss;
-    __syncthreads();
-    const float tot = (red[0] + red[1]) + (red[2] + red[3]);
-    __syncthreads();
-    y = y * rsqrtf(tot * (1.f / W) + a.eps) * (1.f - __ldg(a.lambda_init));
-  }
-  const int64_t off = b * a.os[0] + (int64_t)u * a.os[1] + c;
-  if (mine && in_bounds(off, 1, a.ext_out, a.cache.dev_status, a.cache.dbg_status))
-    static_cast<__nv_bfloat16*>(a.out)[off] = __float2bfloat16_rn(y);
 }
 
 // How the work is dealt out. Entry b has n_b = ceil(kv_len_b / CK) chunks; the chunks of all
@@ -184,37 +196,37 @@ __device__ __forceinline__ uint32_t block_sum(uint32_t v, uint32_t* buf, int war
   return sum;
 }
 
+// The consumers' barrier (the copying warp does not take part).
+template <int THREADS>
+__device__ __forceinline__ void bar_consumers() {
+  asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
+}
+
 template <int NT, int HB, Kv4Load LOAD>
-__global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2)
+__global__ void __launch_bounds__(Tile<NT, HB>::THREADS, Tile<NT, HB>::BLOCKS_PER_SM)
     decode_kv4_split_kernel(const __grid_constant__ CUtensorMap map, DecodeKv4Args a) {
-  using TL = Tile<HB>;
-  constexpr int CK = TL::CK, STAGES = TL::STAGES, PITCH = TL::PITCH, ROWS = 8 * NT;
+  using TL = Tile<NT, HB>;
+  constexpr int CK = TL::CK, STAGES = TL::STAGES, PITCH = TL::PITCH, ROWS = TL::ROWS;
+  constexpr int THREADS = TL::THREADS, WARPS = TL::CW + 1;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint64_t full[STAGES];  // TMA: the chunk of a stage landed
-  __shared__ int readers[STAGES];    // TMA: warps that have read it
-  __shared__ uint32_t bad_rows[STAGES][CK / 32];    // kTmaPaged: rows of a page outside the pool
+  __shared__ uint64_t full[STAGES], empty[STAGES];  // the chunk of a stage has landed; was read
+  __shared__ uint32_t bad_rows[STAGES][CK / 32];    // rows of a chunk of a page outside the pool
   __shared__ int abort_flag;
-  __shared__ float red[4];
   __shared__ uint32_t sums[WARPS];
   __shared__ uint32_t first[2];  // entry of the range's first chunk, chunks before that entry
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int gq = lane >> 2, tq = lane & 3;  // fragment row (or column) and pair index
-  const int hb = warp / TL::PER_HEAD, part = warp % TL::PER_HEAD;  // this warp's head and key part
   const int tiles = (a.group + ROWS - 1) / ROWS;  // of a head's query rows
   const int HQ = a.H / HB * tiles;
   const uint32_t group = blockIdx.x / HQ;
   const int tile_h = blockIdx.x % HQ;
   const int g0 = tile_h / tiles * HB, row0 = tile_h % tiles * ROWS;  // first head, first query row
-  const int g = g0 + hb;
 
-  if constexpr (LOAD != kCopy) {
-    if (tid < STAGES) {
-      mbar_init(&full[tid], 1);
-      readers[tid] = 0;
-    }
-    if (tid == 0) abort_flag = 0;
-    fence_barrier_init();
+  if (tid < STAGES) {
+    mbar_init(&full[tid], 1);
+    mbar_init(&empty[tid], TL::CW);
   }
+  if (tid == 0) abort_flag = 0;
+  fence_barrier_init();
   cudaTriggerProgrammaticLaunchCompletion();
 
   // this block's range and where it begins
@@ -226,18 +238,17 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2)
       T += block_sum(b0 + tid < a.B ? (kv4_len(a, b0 + tid) + CK - 1) / CK : 0, sums, WARPS);
   }
   const Kv4Cuts cuts(T, a.groups);
-  uint32_t at = cuts.begin(group);  // chunk in work
-  const uint32_t range_begin = at, range_end = cuts.begin(group + 1);
+  const uint32_t range_begin = cuts.begin(group), range_end = cuts.begin(group + 1);
   if (group >= min((uint32_t)a.groups, T)) return;
   if (!a.kv_len) {
     const uint32_t n = (a.cache.L + CK - 1) / CK;
     if (tid == 0) {
-      first[0] = at / n;
-      first[1] = at / n * n;
+      first[0] = range_begin / n;
+      first[1] = range_begin / n * n;
     }
   } else {
     uint32_t before = 0;
-    for (int b0 = 0; b0 < a.B && before <= at; b0 += THREADS) {
+    for (int b0 = 0; b0 < a.B && before <= range_begin; b0 += THREADS) {
       const uint32_t n = b0 + tid < a.B ? (kv4_len(a, b0 + tid) + CK - 1) / CK : 0;
       uint32_t scan = n;
 #pragma unroll
@@ -253,7 +264,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2)
         if (w < warp) scan += sums[w];
         before += sums[w];
       }
-      if (scan - n <= at && at < scan) {
+      if (scan - n <= range_begin && range_begin < scan) {
         first[0] = b0 + tid;
         first[1] = scan - n;
       }
@@ -261,479 +272,553 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2)
   }
   __syncthreads();
   int b = (int)first[0];
-  uint32_t entry_begin = first[1];
-
-  const float sl2 = 1.4426950408889634f * (a.v1 ? 0.125f : 0.08838834764831845f);  // log2(e) / sqrt(d)
-  bool bad_page = false;
-  uint32_t used = 0;    // chunks that went through the ring before this entry
-
-  for (;;) {  // one entry, or what of it lies in the range, at a time
-  const int kv_len = kv4_len(a, b);
-  const uint32_t entry_end = entry_begin + (kv_len + CK - 1) / CK;
-  const uint32_t stop = min(entry_end, range_end);
-  const int n_chunks = (int)(stop - at);
-  const int t0 = (int)(at - entry_begin) * CK;  // first token
-
-  // Paged: the pages of a chunk are looked up one chunk ahead of its copies. kTmaPaged: lane i
-  // holds box i's page; kCopy: lane r the byte offset of record r. -1: no key there, -2: a
-  // page outside the pool. Either way the records' scales become zero, so they count as K
-  // and V rows of zeros (and keys past the end get no weight at all).
-  const int box_rows = LOAD == kTmaPaged ? min(1 << a.cache.page_shift, CK) : CK;
-  int64_t ahead = -1;
-  auto lookup = [&](int c) {
-    ahead = -1;
-    if constexpr (LOAD == kTmaPaged) {
-      const int tok = t0 + c * CK + lane * box_rows;
-      if (lane * box_rows < CK && tok < kv_len) {
-        const int64_t bi = (int64_t)b * a.cache.bt_stride + (tok >> a.cache.page_shift);
-        int id = -1;
-        if (in_bounds(bi, 1, a.cache.ext_bt, a.cache.dev_status, a.cache.dbg_status))
-          id = __ldg(a.cache.block_table + bi);
-        ahead = (unsigned)id < (unsigned)a.cache.num_pages ? id : -2;
-      }
-    } else if constexpr (LOAD == kCopy) {
-      const int tok = t0 + c * CK + part * KEYS + lane;
-      if (tok < kv_len) {
-        ahead = kv4_page_offset(a.cache, b, tok);
-        if (ahead < 0) ahead = -2;
-      }
+  uint32_t at = range_begin, entry_begin = first[1];  // chunk in work, first one of its entry
+  int stage = 0;
+  uint32_t parity = 0;  // of the ring's current round
+  auto advance = [&] {
+    if (++stage == STAGES) {
+      stage = 0;
+      parity ^= 1u;
     }
-    bad_page = bad_page || ahead == -2;
   };
-  // The copies of chunk c of this entry into its stage. TMA: by one warp, the first chunks by
-  // warp 0, each later one by the warp that was last to read what the stage held. kCopy: each
-  // warp its own records, eight lanes the 128 code bytes of one, then lane r the scales of
-  // record r.
-  auto load = [&](int c) {
-    const uint32_t ring = used + c;
-    const int s = ring % STAGES;
-    uint8_t* st = smem + s * TL::STAGE_BYTES;
-    if constexpr (LOAD == kCopy) {
-      const int64_t head_off = (int64_t)g * a.cache.stride[2];
-      auto copy = [&](int row, int64_t row_off, int piece) {
-        bool ok = row_off >= 0;
-        const int64_t off = (ok ? row_off : 0) + head_off + piece * 16;
-        ok = ok && in_bounds(off, 16, a.cache.ext, a.cache.dev_status, a.cache.dbg_status);
-        cp_async_16(st + (part * KEYS + row) * PITCH + hb * kKv4Record + piece * 16, a.cache.base + (ok ? off : 0),
-                    ok ? 16u : 0u);
-      };
+
+  if (warp == TL::CW) {
+    // ---- copies: chunk after chunk of the range, through all its entries, as stages are freed
+    uint32_t issued = 0;
+    bool ok = true, bad_page = false;
+    while (ok && at < range_end) {
+      const int kv_len = kv4_len(a, b);
+      const uint32_t entry_end = entry_begin + (kv_len + CK - 1) / CK, stop = min(entry_end, range_end);
+      for (; ok && at < stop; ++at) {
+        const int tok0 = (int)(at - entry_begin) * CK;
+        uint8_t* st = smem + stage * TL::STAGE_BYTES;
+        const int x = HB == 1 ? 0 : g0 * (kKv4Record / 4), y = HB == 1 ? g0 : 0;  // TMA: see kv4_map
+        // The pages first, while the stage may still be in use. Rows of a page outside the pool
+        // are marked and left out: their scales become zero, so they count as K and V of zeros.
+        [[maybe_unused]] const int box_rows = LOAD == kTmaPaged ? min(1 << a.cache.page_shift, CK) : CK;
+        [[maybe_unused]] int page = -1;
+        [[maybe_unused]] int64_t off[CK / 32];
+        [[maybe_unused]] uint32_t bad = 0;
+        if constexpr (LOAD == kTmaPaged) {
+          const int tok = tok0 + lane * box_rows;
+          const bool need = lane * box_rows < CK && tok < kv_len;
+          if (need) {
+            const int64_t bi = (int64_t)b * a.cache.bt_stride + (tok >> a.cache.page_shift);
+            if (in_bounds(bi, 1, a.cache.ext_bt, a.cache.dev_status, a.cache.dbg_status))
+              page = __ldg(a.cache.block_table + bi);
+            if ((unsigned)page >= (unsigned)a.cache.num_pages) page = -1;
+          }
+          bad = __ballot_sync(0xffffffffu, need && page < 0);
+          bad_page = bad_page || bad != 0;
+        } else if constexpr (LOAD == kRows) {
 #pragma unroll
-      for (int it = 0; it < KEYS / 4; ++it) {
-        const int row = it * 4 + (lane >> 3);
-        copy(row, __shfl_sync(0xffffffffu, ahead, row), lane & 7);
+          for (int i = 0; i < CK / 32; ++i) {
+            const int tok = tok0 + i * 32 + lane;
+            off[i] = tok < kv_len ? kv4_page_offset(a.cache, b, tok) : -2;
+            bad_page = bad_page || off[i] == -1;
+            if (off[i] >= 0) {
+              off[i] += (int64_t)g0 * a.cache.stride[2];
+              if (!in_bounds(off[i], HB * kKv4Record, a.cache.ext, a.cache.dev_status, a.cache.dbg_status)) off[i] = -1;
+            }
+          }
+        }
+        if (issued >= (uint32_t)STAGES) {
+          ok = mbar_wait(&empty[stage], parity ^ 1u, &abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+        }
+        if constexpr (LOAD == kTma) {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&full[stage], TL::STAGE_BYTES);
+            tma_load_4d(st, &map, &full[stage], x, y, tok0, b);
+          }
+        } else if constexpr (LOAD == kTmaPaged) {
+          const uint32_t boxes = __ballot_sync(0xffffffffu, page >= 0);
+          if (lane < CK / 32) {  // the bad boxes' rows, 32 to a word
+            uint32_t rows = 0;
+            for (int r = 0; bad && r < 32; r += min(box_rows, 32))
+              if ((bad >> ((lane * 32 + r) / box_rows)) & 1u)
+                rows |= (box_rows >= 32 ? 0xffffffffu : (1u << box_rows) - 1u) << r;
+            bad_rows[stage][lane] = rows;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(&full[stage], __popc(boxes) * box_rows * PITCH);
+          __syncwarp();
+          if (page >= 0)
+            tma_load_4d(st + lane * box_rows * PITCH, &map, &full[stage], x, y,
+                        (tok0 + lane * box_rows) & ((1 << a.cache.page_shift) - 1), page);
+        } else {
+          int rows = 0;
+#pragma unroll
+          for (int i = 0; i < CK / 32; ++i) {
+            rows += __popc(__ballot_sync(0xffffffffu, off[i] >= 0));
+            const uint32_t lost = __ballot_sync(0xffffffffu, off[i] == -1);
+            if (lane == 0) bad_rows[stage][i] = lost;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(&full[stage], rows * HB * kKv4Record);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < CK / 32; ++i)
+            if (off[i] >= 0) bulk_load(st + (i * 32 + lane) * PITCH, a.cache.base + off[i], HB * kKv4Record, &full[stage]);
+        }
+        ++issued;
+        advance();
       }
-      copy(lane, ahead, 8);
-    } else {
-      // HB = 1: one head's records {144 bytes, head, token, entry}; else whole token rows
-      const int x = HB == 1 ? 0 : g0 * (kKv4Record / 4), y = HB == 1 ? g0 : 0;
-      if constexpr (LOAD == kTma) {
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&full[s], TL::STAGE_BYTES);
-          tma_load_4d(st, &map, &full[s], x, y, t0 + c * CK, b);
-        }
-      } else {
-        const uint32_t boxes = __ballot_sync(0xffffffffu, ahead >= 0);
-        const uint32_t bad = __ballot_sync(0xffffffffu, ahead == -2);
-        if (lane < CK / 32) {  // the bad boxes' rows, 32 to a word
-          uint32_t rows = 0;
-          for (int r = 0; r < 32; r += min(box_rows, 32))
-            if ((bad >> ((lane * 32 + r) / box_rows)) & 1u)
-              rows |= (box_rows >= 32 ? 0xffffffffu : (1u << box_rows) - 1u) << r;
-          bad_rows[s][lane] = rows;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(&full[s], __popc(boxes) * box_rows * PITCH);
-        __syncwarp();
-        if (ahead >= 0)
-          tma_load_4d(st + lane * box_rows * PITCH, &map, &full[s], x, y,
-                      (t0 + c * CK + lane * box_rows) & ((1 << a.cache.page_shift) - 1), (int)ahead);
+      if (ok && at < range_end) {
+        entry_begin = entry_end;
+        do ++b;  // the next entry that has keys
+        while (kv4_len(a, b) == 0);
       }
     }
-  };
-
-  constexpr int AHEAD = LOAD == kCopy ? STAGES - 1 : STAGES;  // chunks in flight or in work
-  if (LOAD == kCopy || warp == 0) {
-    for (int c = 0; c < AHEAD; ++c) {
-      if (c < n_chunks) {
-        lookup(c);
-        load(c);
-      }
-      if constexpr (LOAD == kCopy) cp_async_commit();
+    if (bad_page) report_status(a.cache.dev_status, DIFFATTN_ERR_INVALID_ARG);
+    if (!ok) {
+      // the readers gave up: the copies in flight end before the block does
+      const uint32_t from = issued > (uint32_t)STAGES ? issued - STAGES : 0;
+      for (uint32_t i = from; i < issued; ++i) mbar_wait_drain(&full[i % STAGES], (i / STAGES) & 1u);
     }
+    return;
   }
+
+  // ---- compute
+  const int gq = lane >> 2, tq = lane & 3;  // fragment row (or column) and pair index
+  const int hb = warp / TL::PER_HEAD, part = warp % TL::PER_HEAD;  // this warp's head and key part
+  const int g = g0 + hb;
+  const float sl2 = 1.4426950408889634f * (a.v1 ? 0.125f : 0.08838834764831845f);  // log2(e) / sqrt(d)
+  const Magic magic;
   bool ok = true;  // no wait has run out
 
-  // Query fragments (B operands), rows scaled to fp16: for group gr and k-step ks, register 0
-  // holds channels 32 gr + 8 tq + 2 ks + {0, 4}, register 1 the next pair over 16 (the order
-  // in which the nibbles of a word come). Lane column gq; start and factor are per column of
-  // the accumulators, 2 tq and 2 tq + 1.
-  uint32_t qb[NT][8][2];
-  float start[NT][4][4];  // -8 * 2^-24 * sum of the group's q, as accumulators
-  float factor[NT][2];    // accumulated score -> log2 domain
+  for (;;) {  // one entry, or what of it lies in the range, at a time
+    const int kv_len = kv4_len(a, b);
+    const uint32_t entry_end = entry_begin + (kv_len + CK - 1) / CK, stop = min(entry_end, range_end);
+
+    // Query fragments (B operands), rows scaled to fp16: for group gr and k-step ks, register 0
+    // holds channels 32 gr + 8 tq + 2 ks + {0, 4}, register 1 the next pair over 16 (the order
+    // in which the nibbles of a word come). Lane column gq; factor is per column of the
+    // accumulators, 2 tq and 2 tq + 1.
+    uint32_t qb[NT][8][2];
+    uint32_t shift[NT][2];  // the -8 of all nibbles, see the scores below
+    float factor[NT][2];    // accumulated score -> log2 domain
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int row = row0 + nt * 8 + gq;
-    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
-    int64_t off = b * a.qs[0];
-    if (a.v1) off += (int64_t)g * a.qs[1];  // the branches lie side by side in the head's row
-    else off += ((int64_t)g * a.group + row) * a.qs[1];
-    const bool ok = row < a.group && in_bounds(off, W, a.ext_q, a.cache.dev_status, a.cache.dbg_status);
-    uint4 w[4];
-    float top = 0.f;
-    bool odd = false;  // an infinity or a NaN
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = row0 + nt * 8 + gq;
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
+      int64_t off = b * a.qs[0];
+      if (a.v1) off += (int64_t)g * a.qs[1];  // the branches lie side by side in the head's row
+      else off += ((int64_t)g * a.group + row) * a.qs[1];
+      const bool have = row < a.group && in_bounds(off, W, a.ext_q, a.cache.dev_status, a.cache.dbg_status);
+      uint4 w[4];
+      float top = 0.f;
+      bool odd = false;  // an infinity or a NaN
 #pragma unroll
-    for (int gr = 0; gr < 4; ++gr) {
-      // V1: row 0 has only groups 0, 1 (branch 1), row 1 only groups 2, 3 (branch 2)
-      const bool mine = ok && (!a.v1 || (gr >> 1) == row);
-      w[gr] = mine ? *reinterpret_cast<const uint4*>(q + off + gr * 32 + tq * 8) : make_uint4(0u, 0u, 0u, 0u);
-      const uint32_t x[4] = {w[gr].x, w[gr].y, w[gr].z, w[gr].w};
+      for (int gr = 0; gr < 4; ++gr) {
+        // V1: row 0 has only groups 0, 1 (branch 1), row 1 only groups 2, 3 (branch 2)
+        const bool mine = have && (!a.v1 || (gr >> 1) == row);
+        w[gr] = mine ? *reinterpret_cast<const uint4*>(q + off + gr * 32 + tq * 8) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t x[4] = {w[gr].x, w[gr].y, w[gr].z, w[gr].w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        top = fmaxf(top, fmaxf(fabsf(bf16_low(x[i])), fabsf(bf16_high(x[i]))));
-        odd = odd || (x[i] & 0x7f80u) == 0x7f80u || (x[i] & 0x7f800000u) == 0x7f800000u;
+        for (int i = 0; i < 4; ++i) {
+          top = fmaxf(top, fmaxf(fabsf(bf16_low(x[i])), fabsf(bf16_high(x[i]))));
+          odd = odd || (x[i] & 0x7f80u) == 0x7f80u || (x[i] & 0x7f800000u) == 0x7f800000u;
+        }
       }
+#pragma unroll
+      for (int o = 1; o <= 2; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      // exponent field of the row's largest element -> scale 2^(141 - ex), inverse in `factor`
+      const int ex = (int)(__float_as_uint(top) >> 23);
+      const float up = odd ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)min(268 - ex, 254) << 23);
+      float sums_q[4];  // -8 * 2^-24 * sum of the group's q
+#pragma unroll
+      for (int gr = 0; gr < 4; ++gr) {
+        const uint32_t x[4] = {w[gr].x, w[gr].y, w[gr].z, w[gr].w};
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[2 * i] = bf16_low(x[i]) * up;
+          v[2 * i + 1] = bf16_high(x[i]) * up;
+        }
+        float sum = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          qb[nt][2 * gr + ks][0] = pack_f16(v[2 * ks], v[2 * ks + 4]);
+          qb[nt][2 * gr + ks][1] = pack_f16(v[2 * ks + 1] * 0.0625f, v[2 * ks + 5] * 0.0625f);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += v[i];
+#pragma unroll
+        for (int o = 1; o <= 2; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        sums_q[gr] = sum * (-8.f / 16777216.f);
+      }
+      // those sums in three bf16 parts (24 bits): k = 4 part + group of a B operand
+      const float c0 = tq & 1 ? sums_q[2] : sums_q[0], c1 = tq & 1 ? sums_q[3] : sums_q[1];
+      const uint32_t part1 = pack_bf16(c0, c1);
+      const float d0 = c0 - bf16_low(part1), d1 = c1 - bf16_high(part1);
+      const uint32_t part2 = pack_bf16(d0, d1);
+      const uint32_t part3 = pack_bf16(d0 - bf16_low(part2), d1 - bf16_high(part2));
+      shift[nt][0] = tq < 2 ? part1 : part2;
+      shift[nt][1] = tq < 2 ? part3 : 0u;
+      // 2^24 (nibbles as 2^-24) * 2^(ex - 141) * log2(e) / sqrt(d). Rows with elements past
+      // 2^117 overflow here to infinite scores
+      const float down = ldexpf(sl2, 24 - 141 + max(ex, 14));
+#pragma unroll
+      for (int j = 0; j < 2; ++j) factor[nt][j] = __shfl_sync(0xffffffffu, down, (2 * tq + j) * 4);
     }
+
+    // columns 2 tq, 2 tq + 1: the running maximum plus kSlack; kTop - maximum - E, twice; sums of
+    // p over the keys gq and gq + 8 of each 16
+    float limit[NT][2];
+    float2 bias[NT][2], l[NT][2];
+    float bound_E = -90.f;
+    uint32_t scale_bound = 0;  // bf16 bits that no V scale so far passes, twice
+    // [group][tile]: channels 32 g + 4 gq + 2 tile + {0, 1}
+    float o[NT][4][2][4];
 #pragma unroll
-    for (int o = 1; o <= 2; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    // exponent field of the row's largest element -> scale 2^(141 - ex), inverse in `factor`
-    const int ex = (int)(__float_as_uint(top) >> 23);
-    const float up = odd ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)min(268 - ex, 254) << 23);
-    float sums[4];
+    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-    for (int gr = 0; gr < 4; ++gr) {
-      const uint32_t x[4] = {w[gr].x, w[gr].y, w[gr].z, w[gr].w};
-      float v[8];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = bf16_low(x[i]) * up;
-        v[2 * i + 1] = bf16_high(x[i]) * up;
+      for (int j = 0; j < 2; ++j) {
+        limit[nt][j] = -INFINITY;
+        bias[nt][j] = make_float2(0.f, 0.f);
+        l[nt][j] = make_float2(0.f, 0.f);
       }
-      float sum = 0.f;
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        qb[nt][2 * gr + ks][0] = pack_f16(v[2 * ks], v[2 * ks + 4]);
-        qb[nt][2 * gr + ks][1] = pack_f16(v[2 * ks + 1] * 0.0625f, v[2 * ks + 5] * 0.0625f);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum += v[i];
-#pragma unroll
-      for (int o = 1; o <= 2; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      sums[gr] = sum * (-8.f / 16777216.f);
-    }
-    // 2^24 (nibbles as 2^-24) * 2^(ex - 141) * log2(e) / sqrt(d). Rows with elements past
-    // 2^117 overflow here to infinite scores
-    const float down = ldexpf(sl2, 24 - 141 + max(ex, 14));
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int from = (2 * tq + j) * 4;  // a lane of column 2 tq + j
-      factor[nt][j] = __shfl_sync(0xffffffffu, down, from);
 #pragma unroll
       for (int gr = 0; gr < 4; ++gr)
-        start[nt][gr][j] = start[nt][gr][2 + j] = __shfl_sync(0xffffffffu, sums[gr], from);
+#pragma unroll
+        for (int ti = 0; ti < 2; ++ti)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[nt][gr][ti][i] = 0.f;
     }
-  }
 
-  const Magic magic;
-  // columns 2 tq, 2 tq + 1: the running maximum plus kSlack; kTop - maximum - E, twice; sums of
-  // p over the keys gq and gq + 8 of each 16
-  float limit[NT][2];
-  float2 bias[NT][2], l[NT][2];
-  float bound_E = -90.f;
-  uint32_t scale_bound = 0;  // bf16 bits that no V scale so far passes, twice
-  // [group][tile]: channels 32 g + 4 gq + 2 tile + {0, 1}
-  float o[NT][4][2][4];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      limit[nt][j] = -INFINITY;
-      bias[nt][j] = make_float2(0.f, 0.f);
-      l[nt][j] = make_float2(0.f, 0.f);
-    }
-#pragma unroll
-    for (int gr = 0; gr < 4; ++gr)
-#pragma unroll
-      for (int ti = 0; ti < 2; ++ti)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[nt][gr][ti][i] = 0.f;
-  }
-
-  lookup(AHEAD);
-  for (int c = 0; c < n_chunks; ++c) {
-    if constexpr (LOAD == kCopy) {
-      if (c + AHEAD < n_chunks) load(c + AHEAD);
-      cp_async_commit();
-    }
-    const uint32_t ring = used + c;
-    const int stage = ring % STAGES;
-    uint8_t* st = smem + stage * TL::STAGE_BYTES + part * KEYS * PITCH + hb * kKv4Record;  // this warp's records
-    const int left = kv_len - (t0 + c * CK + part * KEYS);  // keys of them that exist
-    if constexpr (LOAD == kCopy) {
-      cp_async_wait<AHEAD>();
-      __syncwarp();
-    } else {
-      ok = ok && mbar_wait(&full[stage], (ring / STAGES) & 1, &abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      uint32_t out = 0;
-      if constexpr (LOAD == kTmaPaged) out = bad_rows[stage][part];
-      if (left < KEYS || out) {  // scales of records that are not there
-        if (lane >= left || ((out >> lane) & 1u))
-          *reinterpret_cast<uint4*>(st + lane * PITCH + kKv4Scales) = make_uint4(0u, 0u, 0u, 0u);
-        fence_proxy_async();  // before a later TMA copy rewrites the stage
-        __syncwarp();
+    int left = kv_len - (int)(at - entry_begin) * CK - part * KEYS;  // keys from this warp's first on
+    for (uint32_t c = at; c < stop; ++c, left -= CK) {
+      if (ok) {
+        ok = mbar_wait(&full[stage], parity, &abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok && lane == 0) report_status(a.cache.dev_status, DIFFATTN_ERR_TIMEOUT);
       }
-    }
-    if (left > 0) {
-    const uint32_t st32 = smem_u32(st);
+      if (ok && left > 0) {
+        uint8_t* st = smem + stage * TL::STAGE_BYTES + part * KEYS * PITCH + hb * kKv4Record;  // this warp's records
+        uint32_t lost = 0;
+        if constexpr (LOAD != kTma) lost = bad_rows[stage][part];
+        if (left < KEYS || lost) {  // scales of records that are not there
+          if (lane >= left || ((lost >> lane) & 1u))
+            *reinterpret_cast<uint4*>(st + lane * PITCH + kKv4Scales) = make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async();  // before a later copy rewrites the stage
+          __syncwarp();
+        }
+        const uint32_t st32 = smem_u32(st) + (((lane >> 3) & 1) * 8 + (lane & 7)) * PITCH + (lane >> 4) * 16;
 
-    // the largest V scales of this lane's record, as magnitudes (bf16 bits are ordered)
-    const uint2 vs = *reinterpret_cast<const uint2*>(st + lane * PITCH + kKv4Scales + 8);
-    const uint32_t big = __vmaxu2(vs.x & 0x7fff7fffu, vs.y & 0x7fff7fffu);
+        [[maybe_unused]] const uint32_t st32_scales = smem_u32(st) + gq * PITCH + kKv4Scales;
 
-    // scores of 2 x 16 keys: x[.][mt][0, 1] key mt * 16 + gq, [2, 3] key + 8, columns 2tq, +1
-    float x[NT][2][4];
-    uint4 scales[2][2];  // of those keys: {K 0 1, K 2 3, V 0 1, V 2 3}
+        // the largest V scales of this lane's record, as magnitudes (bf16 bits are ordered)
+        const uint2 vs = *reinterpret_cast<const uint2*>(st + lane * PITCH + kKv4Scales + 8);
+        const uint32_t big = __vmaxu2(vs.x & 0x7fff7fffu, vs.y & 0x7fff7fffu);
+
+        // scores of 2 x 16 keys: x[.][mt][0, 1] key mt * 16 + gq, [2, 3] key + 8, columns 2tq, +1
+        float x[NT][2][4];
+        // scales of those keys, {groups 0 1, 2 3}; NT = 2 is short of registers and fetches V's later
+        uint2 ks[2][2], vscale[2][2];
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
+        for (int mt = 0; mt < 2; ++mt) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        scales[mt][h] =
-            *reinterpret_cast<const uint4*>(st + (mt * 16 + h * 8 + gq) * PITCH + kKv4Scales);
-      const uint32_t row = st32 + (mt * 16 + ((lane >> 3) & 1) * 8 + (lane & 7)) * PITCH + (lane >> 4) * 16;
-#pragma unroll
-      for (int gp = 0; gp < 2; ++gp) {
-        uint32_t r[4];
-        ldsm4(row + gp * 32, r);
-#pragma unroll
-        for (int gg = 0; gg < 2; ++gg) {
-          const int gr = 2 * gp + gg;
-          const uint32_t lo = r[2 * gg], hi = r[2 * gg + 1], lo8 = lo >> 8, hi8 = hi >> 8;
-          const uint32_t k0 = gp ? scales[mt][0].y : scales[mt][0].x, k1 = gp ? scales[mt][1].y : scales[mt][1].x;
-          const float s0 = gg ? bf16_high(k0) : bf16_low(k0), s1 = gg ? bf16_high(k1) : bf16_low(k1);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float acc[4];
-            mma_f16(acc, nib_even(lo), nib_even(hi), nib_odd(lo), nib_odd(hi), qb[nt][2 * gr][0], qb[nt][2 * gr][1],
-                    start[nt][gr]);
-            mma_f16(acc, nib_even(lo8), nib_even(hi8), nib_odd(lo8), nib_odd(hi8), qb[nt][2 * gr + 1][0],
-                    qb[nt][2 * gr + 1][1], acc);
-            float* xx = x[nt][mt];
-            if (gr == 0) {
-              xx[0] = s0 * acc[0]; xx[1] = s0 * acc[1]; xx[2] = s1 * acc[2]; xx[3] = s1 * acc[3];
+          for (int h = 0; h < 2; ++h) {
+            const uint4* at16 = reinterpret_cast<const uint4*>(st + (mt * 16 + h * 8 + gq) * PITCH + kKv4Scales);
+            if constexpr (NT == 1) {
+              const uint4 both = *at16;
+              ks[mt][h] = make_uint2(both.x, both.y);
+              vscale[mt][h] = make_uint2(both.z, both.w);
             } else {
-              xx[0] = fmaf(s0, acc[0], xx[0]); xx[1] = fmaf(s0, acc[1], xx[1]);
-              xx[2] = fmaf(s1, acc[2], xx[2]); xx[3] = fmaf(s1, acc[3], xx[3]);
+              ks[mt][h] = *reinterpret_cast<const uint2*>(at16);
+            }
+          }
+          // sum over groups of scale * (-8 sum q), as a product of the scales and `shift`
+          const uint32_t k0 = tq & 1 ? ks[mt][0].y : ks[mt][0].x;
+          const uint32_t k1 = tq & 1 ? ks[mt][1].y : ks[mt][1].x;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_bf16(x[nt][mt], k0, k1, k0, k1, shift[nt][0], shift[nt][1]);
+#pragma unroll
+          for (int gp = 0; gp < 2; ++gp) {
+            uint32_t r[4];
+            ldsm4(st32 + mt * 16 * PITCH + gp * 32, r);
+#pragma unroll
+            for (int gg = 0; gg < 2; ++gg) {
+              const int gr = 2 * gp + gg;
+              const uint32_t lo = r[2 * gg], hi = r[2 * gg + 1], lo8 = lo >> 8, hi8 = hi >> 8;
+              const uint32_t w0 = gp ? ks[mt][0].y : ks[mt][0].x, w1 = gp ? ks[mt][1].y : ks[mt][1].x;
+              const float s0 = gg ? bf16_high(w0) : bf16_low(w0), s1 = gg ? bf16_high(w1) : bf16_low(w1);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                float acc[4];
+                mma_f16(acc, nib_even(lo), nib_even(hi), nib_odd(lo), nib_odd(hi), qb[nt][2 * gr][0],
+                        qb[nt][2 * gr][1]);
+                mma_f16(acc, nib_even(lo8), nib_even(hi8), nib_odd(lo8), nib_odd(hi8), qb[nt][2 * gr + 1][0],
+                        qb[nt][2 * gr + 1][1], acc);
+                float* xx = x[nt][mt];
+                xx[0] = fmaf(s0, acc[0], xx[0]); xx[1] = fmaf(s0, acc[1], xx[1]);
+                xx[2] = fmaf(s1, acc[2], xx[2]); xx[3] = fmaf(s1, acc[3], xx[3]);
+              }
+            }
+          }
+        }
+
+        // keys past the end get -inf; does a score or a V scale pass its bound?
+        bool raise = __vmaxu2(big, scale_bound) != scale_bound;
+        float top[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          if (left < KEYS) {
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (mt * 16 + (i >> 1) * 8 + gq >= left) x[nt][mt][i] = -INFINITY;
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            top[nt][j] = factor[nt][j] * fmaxf(fmax3(x[nt][0][j], x[nt][0][2 + j], x[nt][1][j]), x[nt][1][2 + j]);
+            raise = raise || top[nt][j] > limit[nt][j];
+          }
+        }
+        if (__any_sync(0xffffffffu, raise)) {
+          // E: |scale| < 2^E for all V scales so far (not below -90, so that p does not overflow
+          // over rows of zeros)
+          const uint32_t most = __reduce_max_sync(0xffffffffu, max(big & 0xffffu, big >> 16));
+          const float E = fmaxf((float)((int)(most >> 7) - 126), bound_E);
+          bound_E = E;
+          scale_bound = ((uint32_t)((int)E + 126) << 7 | 0x7fu) * 0x10001u;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float t = top[nt][j];
+#pragma unroll
+              for (int s = 4; s <= 16; s <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, s));
+              // what p was weighted with is `bias`, to the last bit: alpha and M go by it
+              const float now = fmaxf(limit[nt][j] - kSlack, t);
+              const float to = now == -INFINITY ? kTop - E : kTop - E - now;
+              const float alpha = limit[nt][j] == -INFINITY ? 0.f : ex2(to - bias[nt][j].x);
+              limit[nt][j] = now + kSlack;
+              bias[nt][j] = make_float2(to, to);
+              l[nt][j].x *= alpha;
+              l[nt][j].y *= alpha;
+#pragma unroll
+              for (int gr = 0; gr < 4; ++gr)
+#pragma unroll
+                for (int ti = 0; ti < 2; ++ti) {
+                  o[nt][gr][ti][j] *= alpha;
+                  o[nt][gr][ti][2 + j] *= alpha;
+                }
+            }
+        }
+        // p of the keys (gq, gq + 8) of each 16, per column
+        float2 p[NT][2][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float2 y = fma2(make_float2(x[nt][mt][j], x[nt][mt][2 + j]),
+                                    make_float2(factor[nt][j], factor[nt][j]), bias[nt][j]);
+              p[nt][mt][j] = make_float2(ex2(y.x), ex2(y.y));
+              l[nt][j] = add2(l[nt][j], p[nt][mt][j]);
+            }
+
+        // O += (p scale)^T-fragments times V
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          if constexpr (NT == 2) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              vscale[mt][h] = lds_uint2(st32_scales + (mt * 16 + h * 8) * PITCH + 8);
+          }
+#pragma unroll
+          for (int gp = 0; gp < 2; ++gp) {
+            uint32_t r[4];
+            ldsm4_t(st32 + kKv4VCodes + mt * 16 * PITCH + gp * 32, r);
+#pragma unroll
+            for (int gg = 0; gg < 2; ++gg) {
+              const int gr = 2 * gp + gg;
+              const uint32_t w0 = gp ? vscale[mt][0].y : vscale[mt][0].x, w1 = gp ? vscale[mt][1].y : vscale[mt][1].x;
+              const float2 s01 = gg ? make_float2(bf16_high(w0), bf16_high(w1)) : make_float2(bf16_low(w0), bf16_low(w1));
+              const uint32_t lo = r[2 * gg], hi = r[2 * gg + 1], lo8 = lo >> 8, hi8 = hi >> 8;
+              const uint32_t a0 = code_even(lo, magic), a1 = code_odd(lo, magic), a2 = code_even(hi, magic),
+                             a3 = code_odd(hi, magic);
+              const uint32_t a4 = code_even(lo8, magic), a5 = code_odd(lo8, magic), a6 = code_even(hi8, magic),
+                             a7 = code_odd(hi8, magic);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                const float2 p0 = mul2(p[nt][mt][0], s01), p1 = mul2(p[nt][mt][1], s01);
+                const uint32_t b0 = transpose8(pack_f16(p0.x, p1.x));
+                const uint32_t b1 = transpose8(pack_f16(p0.y, p1.y));
+                mma_f16(o[nt][gr][0], a0, a1, a2, a3, b0, b1, o[nt][gr][0]);
+                mma_f16(o[nt][gr][1], a4, a5, a6, a7, b0, b1, o[nt][gr][1]);
+              }
             }
           }
         }
       }
+      __syncwarp();  // every lane has read the stage
+      if (lane == 0) mbar_arrive(&empty[stage]);
+      advance();
     }
 
-    // keys past the end get -inf; does a score or a V scale pass its bound?
-    bool raise = __vmaxu2(big, scale_bound) != scale_bound;
-    float top[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      if (left < KEYS) {
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (mt * 16 + (i >> 1) * 8 + gq >= left) x[nt][mt][i] = -INFINITY;
-      }
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        top[nt][j] = factor[nt][j] * fmaxf(fmax3(x[nt][0][j], x[nt][0][2 + j], x[nt][1][j]), x[nt][1][2 + j]);
-        raise = raise || top[nt][j] > limit[nt][j];
-      }
-    }
-    if (__any_sync(0xffffffffu, raise)) {
-      // E: |scale| < 2^E for all V scales so far (not below -90, so that p does not overflow
-      // over rows of zeros)
-      const uint32_t most = __reduce_max_sync(0xffffffffu, max(big & 0xffffu, big >> 16));
-      const float E = fmaxf((float)((int)(most >> 7) - 126), bound_E);
-      bound_E = E;
-      scale_bound = ((uint32_t)((int)E + 126) << 7 | 0x7fu) * 0x10001u;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float t = top[nt][j];
-#pragma unroll
-          for (int s = 4; s <= 16; s <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, s));
-          // what p was weighted with is `bias`, to the last bit: alpha and M go by it
-          const float now = fmaxf(limit[nt][j] - kSlack, t);
-          const float to = now == -INFINITY ? kTop - E : kTop - E - now;
-          const float alpha = limit[nt][j] == -INFINITY ? 0.f : ex2(to - bias[nt][j].x);
-          limit[nt][j] = now + kSlack;
-          bias[nt][j] = make_float2(to, to);
-          l[nt][j].x *= alpha;
-          l[nt][j].y *= alpha;
-#pragma unroll
-          for (int gr = 0; gr < 4; ++gr)
-#pragma unroll
-            for (int ti = 0; ti < 2; ++ti) {
-              o[nt][gr][ti][j] *= alpha;
-              o[nt][gr][ti][2 + j] *= alpha;
-            }
-        }
-    }
-    // p of the keys (gq, gq + 8) of each 16, per column
-    float2 p[NT][2][2];
+    // the sums of p over the warp, and M = -bias (-inf without a key) of the columns
+    float L[NT][2], M[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
+      for (int j = 0; j < 2; ++j) {
+        L[nt][j] = l[nt][j].x + l[nt][j].y;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float2 y = fma2(make_float2(x[nt][mt][j], x[nt][mt][2 + j]),
-                                make_float2(factor[nt][j], factor[nt][j]), bias[nt][j]);
-          p[nt][mt][j] = make_float2(ex2(y.x), ex2(y.y));
-          l[nt][j] = add2(l[nt][j], p[nt][mt][j]);
-        }
-
-    // O += (p scale)^T-fragments times V
+        for (int s = 4; s <= 16; s <<= 1) L[nt][j] += __shfl_xor_sync(0xffffffffu, L[nt][j], s);
+        M[nt][j] = limit[nt][j] == -INFINITY ? -INFINITY : -bias[nt][j].x;
+      }
+    if constexpr (TL::PER_HEAD > 1) {
+      // the head's other warps hand their states to its first
+      constexpr int OTHERS = TL::PER_HEAD - 1;
+      float* sm_o = reinterpret_cast<float*>(smem + STAGES * TL::STAGE_BYTES);  // [HB][OTHERS][ROWS][W]
+      float* sm_ml = sm_o + OTHERS * HB * ROWS * W;                            // [HB][OTHERS][ROWS][2]
+      bar_consumers<TL::CW * 32>();  // the entry before has been joined
+      if (part) {
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-      const uint32_t row = st32 + (mt * 16 + ((lane >> 3) & 1) * 8 + (lane & 7)) * PITCH + kKv4VCodes + (lane >> 4) * 16;
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int gp = 0; gp < 2; ++gp) {
-        uint32_t r[4];
-        ldsm4_t(row + gp * 32, r);
+          for (int j = 0; j < 2; ++j) {
+            const int row = (hb * OTHERS + part - 1) * ROWS + nt * 8 + 2 * tq + j;
+            if (gq == 0) *reinterpret_cast<float2*>(sm_ml + 2 * row) = make_float2(M[nt][j], L[nt][j]);
 #pragma unroll
-        for (int gg = 0; gg < 2; ++gg) {
-          const int gr = 2 * gp + gg;
-          const uint32_t v0 = gp ? scales[mt][0].w : scales[mt][0].z, v1 = gp ? scales[mt][1].w : scales[mt][1].z;
-          const float2 s01 = gg ? make_float2(bf16_high(v0), bf16_high(v1)) : make_float2(bf16_low(v0), bf16_low(v1));
-          const uint32_t lo = r[2 * gg], hi = r[2 * gg + 1], lo8 = lo >> 8, hi8 = hi >> 8;
+            for (int gr = 0; gr < 4; ++gr)
+              *reinterpret_cast<float4*>(sm_o + row * W + gr * 32 + gq * 4) =
+                  make_float4(o[nt][gr][0][j], o[nt][gr][0][2 + j], o[nt][gr][1][j], o[nt][gr][1][2 + j]);
+          }
+      }
+      bar_consumers<TL::CW * 32>();
+      if (part == 0) {
+#pragma unroll 1
+        for (int w = 0; w < OTHERS; ++w)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const float2 w0 = mul2(p[nt][mt][0], s01), w1 = mul2(p[nt][mt][1], s01);
-            const uint32_t b0 = transpose8(pack_f16(w0.x, w1.x));
-            const uint32_t b1 = transpose8(pack_f16(w0.y, w1.y));
-            float(&o0)[4] = o[nt][gr][0];
-            float(&o1)[4] = o[nt][gr][1];
-            mma_f16(o0, code_even(lo, magic), code_odd(lo, magic), code_even(hi, magic), code_odd(hi, magic), b0, b1, o0);
-            mma_f16(o1, code_even(lo8, magic), code_odd(lo8, magic), code_even(hi8, magic), code_odd(hi8, magic), b0, b1, o1);
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int row = (hb * OTHERS + w) * ROWS + nt * 8 + 2 * tq + j;
+              const float2 other = *reinterpret_cast<const float2*>(sm_ml + 2 * row);
+              // a state without keys, or with none above -inf, has M = -inf and nothing to add;
+              // only a NaN among its sums is passed on
+              const float top = fmaxf(M[nt][j], other.x);
+              const float f0 = M[nt][j] == -INFINITY ? 1.f : ex2(M[nt][j] - top);
+              const float f1 = other.x == -INFINITY ? 1.f : ex2(other.x - top);
+              M[nt][j] = top;
+              L[nt][j] = fmaf(L[nt][j], f0, other.y * f1);
+#pragma unroll
+              for (int gr = 0; gr < 4; ++gr) {
+                const float4 v = *reinterpret_cast<const float4*>(sm_o + row * W + gr * 32 + gq * 4);
+                o[nt][gr][0][j] = fmaf(o[nt][gr][0][j], f0, v.x * f1);
+                o[nt][gr][0][2 + j] = fmaf(o[nt][gr][0][2 + j], f0, v.y * f1);
+                o[nt][gr][1][j] = fmaf(o[nt][gr][1][j], f0, v.z * f1);
+                o[nt][gr][1][2 + j] = fmaf(o[nt][gr][1][2 + j], f0, v.w * f1);
+              }
+            }
+      }
+    }
+    if (part == 0) {
+      const bool whole = entry_begin >= range_begin && entry_end <= range_end;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int row = nt * 8 + 2 * tq;  // rows `row`, `row` + 1: the branches of one unit
+        if (whole) {
+          // a unit's 128 channels lie in the 8 lanes of a column pair, 16 to each
+          const bool mine = row0 + row < a.group;
+          const int u = a.v1 ? g : (g * a.group + row0 + row) >> 1;
+          const float lam = mine ? __ldg(a.lambda + u) : 0.f;
+          const float i0 = L[nt][0] == 0.f ? 0.f : __fdiv_rn(1.f, L[nt][0]);
+          const float i1 = L[nt][1] == 0.f ? 0.f : __fdiv_rn(1.f, L[nt][1]);
+          float y[4][4], ss = 0.f;
+#pragma unroll
+          for (int gr = 0; gr < 4; ++gr)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              // rounded alone, so that equal branches with lambda = 1 give exactly 0
+              const float o1 = __fmul_rn(o[nt][gr][i >> 1][2 * (i & 1)], i0);
+              const float o2 = __fmul_rn(o[nt][gr][i >> 1][2 * (i & 1) + 1], i1);
+              y[gr][i] = fmaf(-lam, o2, o1);
+              ss = fmaf(y[gr][i], y[gr][i], ss);
+            }
+          float f = 1.f;
+          if (a.apply_norm) {
+#pragma unroll
+            for (int s = 4; s <= 16; s <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, s);
+            f = rsqrtf(ss * (1.f / W) + a.eps) * (1.f - __ldg(a.lambda_init));
+          }
+          const int64_t off = b * a.os[0] + (int64_t)u * a.os[1] + gq * 4;
+#pragma unroll
+          for (int gr = 0; gr < 4; ++gr)
+            if (mine && in_bounds(off + gr * 32, 4, a.ext_out, a.cache.dev_status, a.cache.dbg_status))
+              *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + off + gr * 32) =
+                  make_uint2(pack_bf16(y[gr][0] * f, y[gr][1] * f), pack_bf16(y[gr][2] * f, y[gr][3] * f));
+        } else {
+          const int slot = entry_begin < range_begin ? 0 : 1;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            if (row0 + row >= a.group) continue;
+            const int64_t rec = (((int64_t)blockIdx.x * 2 + slot) * HB + hb) * ROWS + row + j;
+            if (in_bounds(rec * W, W, a.ext_ws_o, a.cache.dev_status, a.cache.dbg_status)) {
+#pragma unroll
+              for (int gr = 0; gr < 4; ++gr)
+                *reinterpret_cast<float4*>(a.ws_o + rec * W + gr * 32 + gq * 4) =
+                    make_float4(o[nt][gr][0][j], o[nt][gr][0][2 + j], o[nt][gr][1][j], o[nt][gr][1][2 + j]);
+            }
+            if (gq == 0 && in_bounds(rec * 2, 2, a.ext_ws_ml, a.cache.dev_status, a.cache.dbg_status))
+              *reinterpret_cast<float2*>(a.ws_ml + rec * 2) = make_float2(M[nt][j], L[nt][j]);
           }
         }
       }
     }
-    }
-    __syncwarp();  // every lane has read the stage
-    if constexpr (LOAD != kCopy) {
-      int last = 0;
-      if (lane == 0) {
-        asm volatile("atom.acq_rel.cta.shared::cta.add.u32 %0, [%1], 1;" : "=r"(last) : "r"(smem_u32(&readers[stage])) : "memory");
-        last = last == WARPS - 1;
-        if (last) readers[stage] = 0;  // read next by warps that have waited for the next chunk
-      }
-      last = __shfl_sync(0xffffffffu, last, 0);
-      if (last && c + AHEAD < n_chunks) load(c + AHEAD);
-    }
-    lookup(c + AHEAD + 1);
+    at = stop;
+    if (at == range_end) break;
+    entry_begin = entry_end;
+    do ++b;  // the next entry that has keys
+    while (kv4_len(a, b) == 0);
   }
-  if constexpr (LOAD == kCopy) {
-    cp_async_wait<0>();
-  } else if (!__syncthreads_and(ok)) {
-    // a copy that never landed: let the ones in flight finish before the block ends
-    if (tid < STAGES) {
-      const int c = n_chunks <= STAGES ? tid : n_chunks - 1 - (n_chunks - 1 - tid) % STAGES;
-      if (c < n_chunks) mbar_wait_drain(&full[(used + c) % STAGES], ((used + c) / STAGES) & 1);
-    }
-    if (tid == 0) report_status(a.cache.dev_status, DIFFATTN_ERR_TIMEOUT);
-    break;
-  }
-  used += n_chunks;
+}
 
-  // the warps' states, [warp][row][channel] outputs and (M, l), in the ring's memory; then the
-  // warps of a head joined
-  float* sm_o = reinterpret_cast<float*>(smem);
-  float* sm_ml = sm_o + WARPS * ROWS * W;
-  static_assert(WARPS * ROWS * (W + 2) * 4 <= TL::SMEM_BYTES, "the join fits in the ring");
-  __syncthreads();
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int row = warp * ROWS + nt * 8 + 2 * tq + j;
-      float sum = l[nt][j].x + l[nt][j].y;
-#pragma unroll
-      for (int s = 4; s <= 16; s <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-      if (gq == 0) {
-        sm_ml[2 * row] = limit[nt][j] == -INFINITY ? -INFINITY : -bias[nt][j].x;
-        sm_ml[2 * row + 1] = sum;
-      }
-#pragma unroll
-      for (int gr = 0; gr < 4; ++gr)
-        *reinterpret_cast<float4*>(sm_o + row * W + gr * 32 + gq * 4) =
-            make_float4(o[nt][gr][0][j], o[nt][gr][0][2 + j], o[nt][gr][1][j], o[nt][gr][1][2 + j]);
-    }
-  __syncthreads();
-  const bool whole = entry_begin >= range_begin && entry_end <= range_end;
-  const int slot = entry_begin < range_begin ? 0 : 1;
-  const int rows = min(ROWS, a.group - row0);
-  for (int h = 0; h < HB; ++h) {
-    float prev = 0.f;
-    for (int r = 0; r < rows; ++r) {
-      const int from = h * TL::PER_HEAD * ROWS + r;  // the head's first warp; its others ROWS apart
-      float M = -INFINITY, L = 0.f, O = 0.f;
-#pragma unroll
-      for (int w = 0; w < TL::PER_HEAD; ++w) M = fmaxf(M, sm_ml[2 * (from + w * ROWS)]);
-#pragma unroll
-      for (int w = 0; w < TL::PER_HEAD; ++w) {
-        const float mw = sm_ml[2 * (from + w * ROWS)];
-        // a warp without keys, or with none above -inf, has M = -inf and nothing to add; only
-        // a NaN among its sums is passed on
-        const float f = mw == -INFINITY ? 1.f : ex2(mw - M);
-        L = fmaf(sm_ml[2 * (from + w * ROWS) + 1], f, L);
-        O = fmaf(sm_o[(from + w * ROWS) * W + tid], f, O);
-      }
-      if (whole) {
-        const float y = L == 0.f ? 0.f : O / L;
-        const int head = g0 + h;
-        if (r & 1) store_unit(a, b, a.v1 ? head : (head * a.group + row0 + r) >> 1, tid, true, prev, y, red);
-        prev = y;
-      } else {
-        const int64_t rec = (((int64_t)blockIdx.x * 2 + slot) * HB + h) * ROWS + r;
-        if (in_bounds(rec * W + tid, 1, a.ext_ws_o, a.cache.dev_status, a.cache.dbg_status))
-          a.ws_o[rec * W + tid] = O;
-        if (tid == 0 && in_bounds(rec * 2, 2, a.ext_ws_ml, a.cache.dev_status, a.cache.dbg_status)) {
-          a.ws_ml[rec * 2] = M;
-          a.ws_ml[rec * 2 + 1] = L;
-        }
-      }
-    }
+// The output of one unit (V1 head or V2 pair) from its branches' attention outputs, channel
+// `c` of the W threads with `mine`: the difference, and V1's norm and scale. All threads of the
+// block take part; `red` holds 4 floats.
+__device__ __forceinline__ void store_unit(const DecodeKv4Args& a, int b, int u, int c, bool mine, float o1,
+                                           float o2, float* red) {
+  float y = o1 - __ldg(a.lambda + u) * o2;
+  if (a.apply_norm) {
+    const float ss = warp_sum(y * y);
+    if (mine && (c & 31) == 0) red[c >> 5] = ss;
+    __syncthreads();
+    const float tot = (red[0] + red[1]) + (red[2] + red[3]);
+    __syncthreads();
+    y = y * rsqrtf(tot * (1.f / W) + a.eps) * (1.f - __ldg(a.lambda_init));
   }
-  at = stop;
-  if (at == range_end) break;
-  entry_begin = entry_end;
-  do ++b;  // the next entry that has keys
-  while (kv4_len(a, b) == 0);
-  fence_proxy_async();  // the join's stores before the next entry's copies
-  __syncthreads();
-  }
-  if (bad_page) report_status(a.cache.dev_status, DIFFATTN_ERR_INVALID_ARG);
+  const int64_t off = b * a.os[0] + (int64_t)u * a.os[1] + c;
+  if (mine && in_bounds(off, 1, a.ext_out, a.cache.dev_status, a.cache.dbg_status))
+    static_cast<__nv_bfloat16*>(a.out)[off] = __float2bfloat16_rn(y);
 }
 
 // Joins the states of the units that several blocks share, and writes the zero rows of entries
 // without keys: one block per output unit (V1 head or V2 pair) and entry. A state's weight
-// 2^(M_s - M) is computed once by one thread; SLICES threads per value channel then add every
-// SLICES-th state, both rows, and their sums are added in order. (With one thread per channel
-// walking all states the join of 103 of them took 52 us, more than the attention.)
-constexpr int SLICES = 4;
-constexpr int JOIN = 128;  // states whose weights are held at a time
-__global__ void __launch_bounds__(W * SLICES) decode_kv4_combine_kernel(DecodeKv4Args a) {
+// 2^(M_s - M) is computed once by one thread; each of SLICES warps then adds every SLICES-th
+// state, four channels to a lane and both rows, and their sums are added in order. (103 states
+// took 52 us with a thread to a channel walking them all.) SLICES = 16 for few entries with
+// many states each, 4 for many with few: 222 states of one entry took 15 us instead of 32,
+// 10 states each of 24 entries 18 us instead of 29.
+template <int SLICES>
+__global__ void __launch_bounds__(32 * SLICES) decode_kv4_combine_kernel(DecodeKv4Args a) {
+  constexpr int JOIN = 32 * SLICES;  // states whose weights are held at a time
   __shared__ float weight[2][JOIN];
-  __shared__ float part[SLICES][2][W];
-  __shared__ float red[2][W * SLICES / 32];
-  __shared__ uint32_t sums[W * SLICES / 32];
-  constexpr int COMBINE_WARPS = W * SLICES / 32;
-  const int u = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, c = tid % W, slice = tid / W;
+  __shared__ float4 part[SLICES][2][W / 4];
+  __shared__ float red[2][SLICES];
+  __shared__ uint32_t sums[SLICES];
+  constexpr int THREADS = 32 * SLICES;
+  const int u = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // the unit's head, row and head tile
   const int head = a.v1 ? u : 2 * u / a.group, row = 2 * u - head * a.group;
-  const int ck = KEYS * (WARPS / a.heads), per = 8 * a.nt, tiles = (a.group + per - 1) / per;
+  const int ck = KEYS * (compute_warps(a.nt) / a.heads), per = 8 * a.nt, tiles = (a.group + per - 1) / per;
   const int HQ = a.H / a.heads * tiles, tile_h = head / a.heads * tiles + row / per;
   const uint32_t n = (kv4_len(a, b) + ck - 1) / ck;
   uint32_t T, begin;
@@ -742,13 +827,13 @@ __global__ void __launch_bounds__(W * SLICES) decode_kv4_combine_kernel(DecodeKv
     begin = b * n;
   } else {
     uint32_t all = 0, lower = 0;
-    for (int i = tid; i < a.B; i += W * SLICES) {
+    for (int i = tid; i < a.B; i += THREADS) {
       const uint32_t chunks = (kv4_len(a, i) + ck - 1) / ck;
       all += chunks;
       if (i < b) lower += chunks;
     }
-    T = block_sum(all, sums, COMBINE_WARPS);
-    begin = block_sum(lower, sums, COMBINE_WARPS);
+    T = block_sum(all, sums, SLICES);
+    begin = block_sum(lower, sums, SLICES);
   }
   const Kv4Cuts cuts(T, a.groups);
   const uint32_t i0 = n ? cuts.range_of(begin) : 0, i1 = n ? cuts.range_of(begin + n - 1) : 0;
@@ -765,65 +850,77 @@ __global__ void __launch_bounds__(W * SLICES) decode_kv4_combine_kernel(DecodeKv
        in_bounds(record(splits - 1) * W, 2 * W, a.ext_ws_o, a.cache.dev_status, a.cache.dbg_status));
   const int have = ok ? splits : 0;
 
+  // (M, sum) of both rows of state s
+  auto state = [&](int s) { return *reinterpret_cast<const float4*>(a.ws_ml + 2 * record(s)); };
   float M[2] = {-INFINITY, -INFINITY};
-  for (int s = tid; s < have; s += W * SLICES)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) M[e] = fmaxf(M[e], a.ws_ml[2 * (record(s) + e)]);
+  for (int s = tid; s < have; s += THREADS) {
+    const float4 v = state(s);
+    M[0] = fmaxf(M[0], v.x);
+    M[1] = fmaxf(M[1], v.z);
+  }
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     M[e] = warp_max(M[e]);
-    if ((tid & 31) == 0) red[e][tid >> 5] = M[e];
+    if (lane == 0) red[e][warp] = M[e];
   }
   __syncthreads();
 #pragma unroll
   for (int e = 0; e < 2; ++e)
 #pragma unroll
-    for (int w = 0; w < W * SLICES / 32; ++w) M[e] = fmaxf(M[e], red[e][w]);
+    for (int w = 0; w < SLICES; ++w) M[e] = fmaxf(M[e], red[e][w]);
 
-  float L = 0.f, O[2] = {0.f, 0.f};  // threads 0 .. 2 JOIN - 1: row tid / JOIN's sums
+  float L[2] = {0.f, 0.f};
+  float4 O[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
   for (int s0 = 0; s0 < have; s0 += JOIN) {
     const int held = min(JOIN, have - s0);
     __syncthreads();
-    if (tid < 2 * JOIN && tid % JOIN < held) {
-      const int e = tid / JOIN, s = tid % JOIN;
-      const float2 v = *reinterpret_cast<const float2*>(a.ws_ml + 2 * (record(s0 + s) + e));
+    if (tid < held) {
+      const float4 v = state(s0 + tid);
       // a state without keys has M = -inf and nothing to add; only a NaN is passed on
-      const float f = v.x == -INFINITY ? 1.f : ex2(v.x - (e ? M[1] : M[0]));
-      weight[e][s] = f;
-      L = fmaf(v.y, f, L);
+      const float f0 = v.x == -INFINITY ? 1.f : ex2(v.x - M[0]), f1 = v.z == -INFINITY ? 1.f : ex2(v.z - M[1]);
+      weight[0][tid] = f0;
+      weight[1][tid] = f1;
+      L[0] = fmaf(v.y, f0, L[0]);
+      L[1] = fmaf(v.w, f1, L[1]);
     }
     __syncthreads();
 #pragma unroll 4
-    for (int s = slice; s < held; s += SLICES) {
-      const float* po = a.ws_o + record(s0 + s) * W + c;
-      O[0] = fmaf(po[0], weight[0][s], O[0]);
-      O[1] = fmaf(po[W], weight[1][s], O[1]);
+    for (int s = warp; s < held; s += SLICES) {
+      const float4* po = reinterpret_cast<const float4*>(a.ws_o + record(s0 + s) * W) + lane;
+      const float4 v0 = po[0], v1 = po[W / 4];
+      const float f0 = weight[0][s], f1 = weight[1][s];
+      O[0] = make_float4(fmaf(v0.x, f0, O[0].x), fmaf(v0.y, f0, O[0].y), fmaf(v0.z, f0, O[0].z), fmaf(v0.w, f0, O[0].w));
+      O[1] = make_float4(fmaf(v1.x, f1, O[1].x), fmaf(v1.y, f1, O[1].y), fmaf(v1.z, f1, O[1].z), fmaf(v1.w, f1, O[1].w));
     }
   }
-  L = warp_sum(L);
   __syncthreads();
-  if ((tid & 31) == 0) red[0][tid >> 5] = L;
-  part[slice][0][c] = O[0];
-  part[slice][1][c] = O[1];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    L[e] = warp_sum(L[e]);
+    if (lane == 0) red[e][warp] = L[e];
+    part[warp][e][lane] = O[e];
+  }
   __syncthreads();
+  const int c = tid % W;  // the first W threads finish, a channel each
   float res[2];
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     float l = 0.f, o = 0.f;
-#pragma unroll
-    for (int w = 0; w < JOIN / 32; ++w) l += red[0][e * (JOIN / 32) + w];
-#pragma unroll
-    for (int i = 0; i < SLICES; ++i) o += part[i][e][c];
+    for (int w = 0; w < SLICES; ++w) {
+      l += red[e][w];
+      o += reinterpret_cast<const float*>(part[w][e])[c];
+    }
     res[e] = l == 0.f ? 0.f : o / l;
   }
-  store_unit(a, b, u, c, slice == 0, res[0], res[1], red[1]);
+  __syncthreads();
+  store_unit(a, b, u, c, tid < W, res[0], res[1], red[0]);
 }
 
 // Heads of a block: neighbours read together (one run of 144 HB bytes per token) when the
 // cache keeps them side by side. On the full-size step copies alone took 430 us with runs of
 // 144 bytes, 390 with 288 and 371 with 576 (the cache once at 6.5 TB/s).
-static int kv4_heads(int H, int64_t head_stride, bool copy) {
-  if (copy || (H > 1 && head_stride != kKv4Record)) return 1;
+static int kv4_heads(int H, int64_t head_stride) {
+  if (H > 1 && head_stride != kKv4Record) return 1;
   return H % 4 == 0 ? 4 : (H % 2 == 0 ? 2 : 1);
 }
 
@@ -832,13 +929,12 @@ static int kv4_heads(int H, int64_t head_stride, bool copy) {
 // kMin. States are kept for two entries of every block.
 void decode_kv4_plan(DecodeKv4Args* a, int num_splits) {
   constexpr int64_t kMin = 2;
-  const int page = 1 << a->cache.page_shift;
   a->nt = a->group > 8 ? 2 : 1;
-  a->heads = kv4_heads(a->H, a->cache.stride[2], a->cache.num_pages > 0 && page < 8);
-  const int64_t ck = KEYS * (WARPS / a->heads);
+  a->heads = kv4_heads(a->H, a->cache.stride[2]);
+  const int64_t ck = KEYS * (compute_warps(a->nt) / a->heads);
   const int64_t HQ = a->H / a->heads * ((a->group + 8 * a->nt - 1) / (8 * a->nt));
   a->chunks = (int64_t)a->B * ((a->cache.L + ck - 1) / ck);
-  int64_t groups = num_splits ? (int64_t)num_splits * a->B : 148 * (a->nt == 1 ? 3 : 2) / HQ;
+  int64_t groups = num_splits ? (int64_t)num_splits * a->B : 148 * (a->nt == 1 ? 3 : 1) / HQ;
   const int64_t most = num_splits ? a->chunks : (a->chunks + kMin - 1) / kMin;
   if (groups > most) groups = most;
   if (groups > (1 << 16)) groups = 1 << 16;
@@ -850,7 +946,7 @@ void decode_kv4_plan(DecodeKv4Args* a, int num_splits) {
 // HB = 1: {144 bytes, heads, rows, entries or pages}, boxes of one head's records; else
 // {bytes of a token's heads, 1, rows, entries or pages}, boxes of HB heads' records and 16
 // bytes (zeros behind the last head). 4-byte elements. False where TMA does not take the strides.
-template <int HB>
+template <int NT, int HB>
 static bool kv4_map(CUtensorMap* m, const Kv4Cache& c, int H, int rows, int outer, int box) {
   auto fn = encode_fn();
   if (!fn || rows < 1) return false;
@@ -863,7 +959,7 @@ static bool kv4_map(CUtensorMap* m, const Kv4Cache& c, int H, int rows, int oute
   if (HB != 1) hs = (int64_t)inner * 4;
   const cuuint64_t dims[4] = {(cuuint64_t)inner, (cuuint64_t)(HB == 1 ? H : 1), (cuuint64_t)rows, (cuuint64_t)outer};
   const cuuint64_t strides[3] = {(cuuint64_t)hs, (cuuint64_t)ts, (cuuint64_t)os};
-  const cuuint32_t boxes[4] = {(cuuint32_t)Tile<HB>::PITCH / 4, 1, (cuuint32_t)box, 1};
+  const cuuint32_t boxes[4] = {(cuuint32_t)Tile<NT, HB>::PITCH / 4, 1, (cuuint32_t)box, 1};
   const cuuint32_t steps[4] = {1, 1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, c.base, dims, strides, boxes, steps,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -872,19 +968,19 @@ static bool kv4_map(CUtensorMap* m, const Kv4Cache& c, int H, int rows, int oute
 
 template <int NT, int HB>
 static cudaError_t launch_split(const DecodeKv4Args& a, cudaStream_t stream) {
-  using TL = Tile<HB>;
+  using TL = Tile<NT, HB>;
   const bool paged = a.cache.block_table != nullptr;
   const int page = 1 << a.cache.page_shift;
   CUtensorMap map;
   memset(&map, 0, sizeof(map));
-  Kv4Load how = kCopy;
-  if (!paged && kv4_map<HB>(&map, a.cache, a.H, a.cache.L, a.B, TL::CK)) how = kTma;
+  Kv4Load how = kRows;
+  if (!paged && kv4_map<NT, HB>(&map, a.cache, a.H, a.cache.L, a.B, TL::CK)) how = kTma;
   if (paged && page >= 8 &&
-      kv4_map<HB>(&map, a.cache, a.H, page, a.cache.num_pages, page < TL::CK ? page : TL::CK))
+      kv4_map<NT, HB>(&map, a.cache, a.H, page, a.cache.num_pages, page < TL::CK ? page : TL::CK))
     how = kTmaPaged;
   void (*const fns[3])(CUtensorMap, DecodeKv4Args) = {decode_kv4_split_kernel<NT, HB, kTma>,
                                                       decode_kv4_split_kernel<NT, HB, kTmaPaged>,
-                                                      decode_kv4_split_kernel<NT, HB, kCopy>};
+                                                      decode_kv4_split_kernel<NT, HB, kRows>};
   void (*const fn)(CUtensorMap, DecodeKv4Args) = fns[how];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -895,7 +991,7 @@ static cudaError_t launch_split(const DecodeKv4Args& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_set[how][dev] = true;
   }
-  fn<<<(unsigned)a.blocks, THREADS, TL::SMEM_BYTES, stream>>>(map, a);
+  fn<<<(unsigned)a.blocks, TL::THREADS, TL::SMEM_BYTES, stream>>>(map, a);
   return cudaGetLastError();
 }
 
@@ -913,11 +1009,12 @@ cudaError_t launch_decode_kv4(const DecodeKv4Args& a, cudaStream_t stream) {
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = dim3(a.H * a.group / 2, a.B);
-  cfg.blockDim = dim3(W * SLICES);
+  const bool many = a.groups > 64 * (int64_t)a.B;
+  cfg.blockDim = dim3(many ? 512 : 128);
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_kv4_combine_kernel, a);
+  return cudaLaunchKernelEx(&cfg, many ? decode_kv4_combine_kernel<16> : decode_kv4_combine_kernel<4>, a);
 }
 
 }  // namespace diffattn

@@ -151,10 +151,11 @@ def test_decode_pointers_norm_and_workspace(lib):
         assert n.value == blocks * 2 * 4 * 8 * 130 * 4, (splits, L)
     p = _params(max_kv_len=1 << 20, kv_strides=(4 * REC << 20, 4 * REC, REC), n_q_heads=64)
     assert size(ctypes.byref(p), None, ctypes.byref(n)) == 0 and n.value < 20 << 20
-    # the pool's geometry takes part: pages under 8 tokens take one head to a block
+    # the layout takes part: heads that do not lie side by side go one to a block
     assert size(ctypes.byref(_params()), ctypes.byref(_pool()), ctypes.byref(n)) == 0
     assert n.value == 2 * 2 * 4 * 8 * 130 * 4
-    assert size(ctypes.byref(_params()), ctypes.byref(_pool(page_size=4, max_pages_per_seq=16)), ctypes.byref(n)) == 0
+    apart = _pool(page_strides=(16 * 4 * 160, 4 * 160, 160))
+    assert size(ctypes.byref(_params()), ctypes.byref(apart), ctypes.byref(n)) == 0
     assert n.value == 4 * 2 * 1 * 8 * 130 * 4
     p = _params()
     assert size(ctypes.byref(p), None, ctypes.byref(n)) == 0
