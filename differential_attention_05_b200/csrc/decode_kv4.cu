@@ -48,31 +48,28 @@ constexpr int KEYS = 32;      // keys that a warp takes of a chunk
 constexpr float kTop = 8.f;   // p * scale <= 2^kTop when the maximum is raised ...
 constexpr float kSlack = 7.f; // ... and <= 2^(kTop + kSlack) before
 
-// A block has CW warps that compute and one that issues the copies: with NT = 1 (up to 8 query
-// rows) 4 of them, three blocks to an SM; with NT = 2 the accumulators of 16 rows need twice
-// the registers, and one block of 8 has an SM to itself.
-constexpr int compute_warps(int nt) { return nt == 1 ? 4 : 8; }
+// A block has CW warps that compute and one that issues the copies; three blocks to an SM.
+constexpr int CW = 4;
+constexpr int THREADS = (CW + 1) * 32;
+constexpr int ROWS = 8;       // query rows of a block, the columns of its MMAs
+constexpr int kBlocksPerSm = 3;
 
 // A block takes HB neighbouring KV heads, CW / HB warps for each. A chunk is CK tokens in a
 // stage of one row per token: the HB records side by side, as they lie in the cache, and 16
 // bytes more (of the next record, unused) where that is needed for a pitch that is an odd
 // number of 16-byte units, so that ldmatrix's 8 rows meet no bank twice.
-template <int NT, int HB>
+template <int HB>
 struct Tile {
-  static constexpr int CW = compute_warps(NT);
-  static constexpr int THREADS = (CW + 1) * 32;
-  static constexpr int BLOCKS_PER_SM = NT == 1 ? 3 : 1;
   static constexpr int PER_HEAD = CW / HB;  // warps of a head
   static constexpr int CK = KEYS * PER_HEAD;
   static constexpr int PITCH = HB * kKv4Record + (HB == 1 ? 0 : 16);
   static constexpr int STAGE_BYTES = CK * PITCH;
   // what shared memory holds beside the states that the warps of a head join at the end
-  static constexpr int STAGES = NT == 1 ? (HB == 4 ? 4 : 3) : (HB == 4 ? 5 : 4);
-  static constexpr int ROWS = 8 * NT;
+  static constexpr int STAGES = HB == 4 ? 4 : 3;
   static constexpr int JOIN_FLOATS = (PER_HEAD - 1) * HB * ROWS * (W + 2);
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + JOIN_FLOATS * 4;
   static_assert((PITCH / 16) % 2 == 1 && STAGE_BYTES % 128 == 0 && 8 * PITCH % 128 == 0, "layout");
-  static_assert(BLOCKS_PER_SM * (SMEM_BYTES + 2048) <= 228 * 1024 && SMEM_BYTES <= 227 * 1024, "shared memory");
+  static_assert(kBlocksPerSm * (SMEM_BYTES + 2048) <= 228 * 1024, "shared memory");
 };
 
 // How a chunk reaches shared memory: TMA boxes of CK rows (contiguous) or of a page's run of
@@ -147,12 +144,6 @@ __device__ __forceinline__ uint32_t code_odd(uint32_t w, const Magic& k) {
   const __half2 y = __hfma2(and_or(w, k.odd, k.magic), __float2half2_rn(0.0625f), __float2half2_rn(-72.f));
   return *reinterpret_cast<const uint32_t*>(&y);
 }
-// a load that stays where it is written
-__device__ __forceinline__ uint2 lds_uint2(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
-  return v;
-}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -161,8 +152,10 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 // How the work is dealt out. Entry b has n_b = ceil(kv_len_b / CK) chunks; the chunks of all
 // entries in a row, T of them, are cut into G = min(groups, T) ranges that differ by at most
 // one chunk, whatever the lengths; a group of blocks takes a range, one block for each head
-// tile (HB heads and up to 8 NT query rows), so that blocks that run side by side read
-// neighbouring heads of the same tokens. (With each block's range in one head tile only, the
+// tile (HB heads and up to 8 query rows of each), so that blocks that run side by side read
+// neighbouring heads of the same tokens. (More than 8 query rows to a head take another tile,
+// which reads the records again, mostly from L2. With 16 rows in a block the accumulators left
+// one block of 8 warps to an SM: 16 rows over 32 x 8192 tokens x 2 heads took 57 us, not 43.) (With each block's range in one head tile only, the
 // copies of the full-size step alone took 473 us instead of 371.) A block finishes the entries
 // that lie within its range and leaves states for the others in the workspace: slot 0 for the
 // entry that began before its range, slot 1 for the one that goes on after it.
@@ -202,12 +195,11 @@ __device__ __forceinline__ void bar_consumers() {
   asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
 }
 
-template <int NT, int HB, Kv4Load LOAD>
-__global__ void __launch_bounds__(Tile<NT, HB>::THREADS, Tile<NT, HB>::BLOCKS_PER_SM)
+template <int HB, Kv4Load LOAD>
+__global__ void __launch_bounds__(THREADS, kBlocksPerSm)
     decode_kv4_split_kernel(const __grid_constant__ CUtensorMap map, DecodeKv4Args a) {
-  using TL = Tile<NT, HB>;
-  constexpr int CK = TL::CK, STAGES = TL::STAGES, PITCH = TL::PITCH, ROWS = TL::ROWS;
-  constexpr int THREADS = TL::THREADS, WARPS = TL::CW + 1;
+  using TL = Tile<HB>;
+  constexpr int CK = TL::CK, STAGES = TL::STAGES, PITCH = TL::PITCH, WARPS = CW + 1;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[STAGES], empty[STAGES];  // the chunk of a stage has landed; was read
   __shared__ uint32_t bad_rows[STAGES][CK / 32];    // rows of a chunk of a page outside the pool
@@ -223,7 +215,7 @@ __global__ void __launch_bounds__(Tile<NT, HB>::THREADS, Tile<NT, HB>::BLOCKS_PE
 
   if (tid < STAGES) {
     mbar_init(&full[tid], 1);
-    mbar_init(&empty[tid], TL::CW);
+    mbar_init(&empty[tid], CW);
   }
   if (tid == 0) abort_flag = 0;
   fence_barrier_init();
@@ -282,7 +274,7 @@ __global__ void __launch_bounds__(Tile<NT, HB>::THREADS, Tile<NT, HB>::BLOCKS_PE
     }
   };
 
-  if (warp == TL::CW) {
+  if (warp == CW) {
     // ---- copies: chunk after chunk of the range, through all its entries, as stages are freed
     uint32_t issued = 0;
     bool ok = true, bad_page = false;
@@ -396,97 +388,91 @@ __global__ void __launch_bounds__(Tile<NT, HB>::THREADS, Tile<NT, HB>::BLOCKS_PE
     // holds channels 32 gr + 8 tq + 2 ks + {0, 4}, register 1 the next pair over 16 (the order
     // in which the nibbles of a word come). Lane column gq; factor is per column of the
     // accumulators, 2 tq and 2 tq + 1.
-    uint32_t qb[NT][8][2];
-    uint32_t shift[NT][2];  // the -8 of all nibbles, see the scores below
-    float factor[NT][2];    // accumulated score -> log2 domain
+    uint32_t qb[8][2];
+    uint32_t shift[2];  // the -8 of all nibbles, see the scores below
+    float factor[2];    // accumulated score -> log2 domain
+    const int row = row0 + gq;
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
+    int64_t off = b * a.qs[0];
+    if (a.v1) off += (int64_t)g * a.qs[1];  // the branches lie side by side in the head's row
+    else off += ((int64_t)g * a.group + row) * a.qs[1];
+    const bool have = row < a.group && in_bounds(off, W, a.ext_q, a.cache.dev_status, a.cache.dbg_status);
+    uint4 w[4];
+    float top = 0.f;
+    bool odd = false;  // an infinity or a NaN
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int row = row0 + nt * 8 + gq;
-      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
-      int64_t off = b * a.qs[0];
-      if (a.v1) off += (int64_t)g * a.qs[1];  // the branches lie side by side in the head's row
-      else off += ((int64_t)g * a.group + row) * a.qs[1];
-      const bool have = row < a.group && in_bounds(off, W, a.ext_q, a.cache.dev_status, a.cache.dbg_status);
-      uint4 w[4];
-      float top = 0.f;
-      bool odd = false;  // an infinity or a NaN
+    for (int gr = 0; gr < 4; ++gr) {
+      // V1: row 0 has only groups 0, 1 (branch 1), row 1 only groups 2, 3 (branch 2)
+      const bool mine = have && (!a.v1 || (gr >> 1) == row);
+      w[gr] = mine ? *reinterpret_cast<const uint4*>(q + off + gr * 32 + tq * 8) : make_uint4(0u, 0u, 0u, 0u);
+      const uint32_t x[4] = {w[gr].x, w[gr].y, w[gr].z, w[gr].w};
 #pragma unroll
-      for (int gr = 0; gr < 4; ++gr) {
-        // V1: row 0 has only groups 0, 1 (branch 1), row 1 only groups 2, 3 (branch 2)
-        const bool mine = have && (!a.v1 || (gr >> 1) == row);
-        w[gr] = mine ? *reinterpret_cast<const uint4*>(q + off + gr * 32 + tq * 8) : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t x[4] = {w[gr].x, w[gr].y, w[gr].z, w[gr].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          top = fmaxf(top, fmaxf(fabsf(bf16_low(x[i])), fabsf(bf16_high(x[i]))));
-          odd = odd || (x[i] & 0x7f80u) == 0x7f80u || (x[i] & 0x7f800000u) == 0x7f800000u;
-        }
+      for (int i = 0; i < 4; ++i) {
+        top = fmaxf(top, fmaxf(fabsf(bf16_low(x[i])), fabsf(bf16_high(x[i]))));
+        odd = odd || (x[i] & 0x7f80u) == 0x7f80u || (x[i] & 0x7f800000u) == 0x7f800000u;
       }
-#pragma unroll
-      for (int o = 1; o <= 2; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      // exponent field of the row's largest element -> scale 2^(141 - ex), inverse in `factor`
-      const int ex = (int)(__float_as_uint(top) >> 23);
-      const float up = odd ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)min(268 - ex, 254) << 23);
-      float sums_q[4];  // -8 * 2^-24 * sum of the group's q
-#pragma unroll
-      for (int gr = 0; gr < 4; ++gr) {
-        const uint32_t x[4] = {w[gr].x, w[gr].y, w[gr].z, w[gr].w};
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[2 * i] = bf16_low(x[i]) * up;
-          v[2 * i + 1] = bf16_high(x[i]) * up;
-        }
-        float sum = 0.f;
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          qb[nt][2 * gr + ks][0] = pack_f16(v[2 * ks], v[2 * ks + 4]);
-          qb[nt][2 * gr + ks][1] = pack_f16(v[2 * ks + 1] * 0.0625f, v[2 * ks + 5] * 0.0625f);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum += v[i];
-#pragma unroll
-        for (int o = 1; o <= 2; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        sums_q[gr] = sum * (-8.f / 16777216.f);
-      }
-      // those sums in three bf16 parts (24 bits): k = 4 part + group of a B operand
-      const float c0 = tq & 1 ? sums_q[2] : sums_q[0], c1 = tq & 1 ? sums_q[3] : sums_q[1];
-      const uint32_t part1 = pack_bf16(c0, c1);
-      const float d0 = c0 - bf16_low(part1), d1 = c1 - bf16_high(part1);
-      const uint32_t part2 = pack_bf16(d0, d1);
-      const uint32_t part3 = pack_bf16(d0 - bf16_low(part2), d1 - bf16_high(part2));
-      shift[nt][0] = tq < 2 ? part1 : part2;
-      shift[nt][1] = tq < 2 ? part3 : 0u;
-      // 2^24 (nibbles as 2^-24) * 2^(ex - 141) * log2(e) / sqrt(d). Rows with elements past
-      // 2^117 overflow here to infinite scores
-      const float down = ldexpf(sl2, 24 - 141 + max(ex, 14));
-#pragma unroll
-      for (int j = 0; j < 2; ++j) factor[nt][j] = __shfl_sync(0xffffffffu, down, (2 * tq + j) * 4);
     }
+#pragma unroll
+    for (int o = 1; o <= 2; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    // exponent field of the row's largest element -> scale 2^(141 - ex), inverse in `factor`
+    const int ex = (int)(__float_as_uint(top) >> 23);
+    const float up = odd ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)min(268 - ex, 254) << 23);
+    float sums_q[4];  // -8 * 2^-24 * sum of the group's q
+#pragma unroll
+    for (int gr = 0; gr < 4; ++gr) {
+      const uint32_t x[4] = {w[gr].x, w[gr].y, w[gr].z, w[gr].w};
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = bf16_low(x[i]) * up;
+        v[2 * i + 1] = bf16_high(x[i]) * up;
+      }
+      float sum = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        qb[2 * gr + ks][0] = pack_f16(v[2 * ks], v[2 * ks + 4]);
+        qb[2 * gr + ks][1] = pack_f16(v[2 * ks + 1] * 0.0625f, v[2 * ks + 5] * 0.0625f);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += v[i];
+#pragma unroll
+      for (int o = 1; o <= 2; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      sums_q[gr] = sum * (-8.f / 16777216.f);
+    }
+    // those sums in three bf16 parts (24 bits): k = 4 part + group of a B operand
+    const float c0 = tq & 1 ? sums_q[2] : sums_q[0], c1 = tq & 1 ? sums_q[3] : sums_q[1];
+    const uint32_t part1 = pack_bf16(c0, c1);
+    const float d0 = c0 - bf16_low(part1), d1 = c1 - bf16_high(part1);
+    const uint32_t part2 = pack_bf16(d0, d1);
+    const uint32_t part3 = pack_bf16(d0 - bf16_low(part2), d1 - bf16_high(part2));
+    shift[0] = tq < 2 ? part1 : part2;
+    shift[1] = tq < 2 ? part3 : 0u;
+    // 2^24 (nibbles as 2^-24) * 2^(ex - 141) * log2(e) / sqrt(d). Rows with elements past
+    // 2^117 overflow here to infinite scores
+    const float down = ldexpf(sl2, 24 - 141 + max(ex, 14));
+#pragma unroll
+    for (int j = 0; j < 2; ++j) factor[j] = __shfl_sync(0xffffffffu, down, (2 * tq + j) * 4);
 
     // columns 2 tq, 2 tq + 1: the running maximum plus kSlack; kTop - maximum - E, twice; sums of
     // p over the keys gq and gq + 8 of each 16
-    float limit[NT][2];
-    float2 bias[NT][2], l[NT][2];
+    float limit[2];
+    float2 bias[2], l[2];
     float bound_E = -90.f;
     uint32_t scale_bound = 0;  // bf16 bits that no V scale so far passes, twice
     // [group][tile]: channels 32 g + 4 gq + 2 tile + {0, 1}
-    float o[NT][4][2][4];
+    float o[4][2][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        limit[nt][j] = -INFINITY;
-        bias[nt][j] = make_float2(0.f, 0.f);
-        l[nt][j] = make_float2(0.f, 0.f);
-      }
-#pragma unroll
-      for (int gr = 0; gr < 4; ++gr)
-#pragma unroll
-        for (int ti = 0; ti < 2; ++ti)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[nt][gr][ti][i] = 0.f;
+    for (int j = 0; j < 2; ++j) {
+      limit[j] = -INFINITY;
+      bias[j] = make_float2(0.f, 0.f);
+      l[j] = make_float2(0.f, 0.f);
     }
+#pragma unroll
+    for (int gr = 0; gr < 4; ++gr)
+#pragma unroll
+      for (int ti = 0; ti < 2; ++ti)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[gr][ti][i] = 0.f;
 
     int left = kv_len - (int)(at - entry_begin) * CK - part * KEYS;  // keys from this warp's first on
     for (uint32_t c = at; c < stop; ++c, left -= CK) {
@@ -507,34 +493,26 @@ __global__ void __launch_bounds__(Tile<NT, HB>::THREADS, Tile<NT, HB>::BLOCKS_PE
         }
         const uint32_t st32 = smem_u32(st) + (((lane >> 3) & 1) * 8 + (lane & 7)) * PITCH + (lane >> 4) * 16;
 
-        [[maybe_unused]] const uint32_t st32_scales = smem_u32(st) + gq * PITCH + kKv4Scales;
-
         // the largest V scales of this lane's record, as magnitudes (bf16 bits are ordered)
         const uint2 vs = *reinterpret_cast<const uint2*>(st + lane * PITCH + kKv4Scales + 8);
         const uint32_t big = __vmaxu2(vs.x & 0x7fff7fffu, vs.y & 0x7fff7fffu);
 
         // scores of 2 x 16 keys: x[.][mt][0, 1] key mt * 16 + gq, [2, 3] key + 8, columns 2tq, +1
-        float x[NT][2][4];
-        // scales of those keys, {groups 0 1, 2 3}; NT = 2 is short of registers and fetches V's later
+        float x[2][4];
+        // scales of those keys, {groups 0 1, 2 3}
         uint2 ks[2][2], vscale[2][2];
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint4* at16 = reinterpret_cast<const uint4*>(st + (mt * 16 + h * 8 + gq) * PITCH + kKv4Scales);
-            if constexpr (NT == 1) {
-              const uint4 both = *at16;
-              ks[mt][h] = make_uint2(both.x, both.y);
-              vscale[mt][h] = make_uint2(both.z, both.w);
-            } else {
-              ks[mt][h] = *reinterpret_cast<const uint2*>(at16);
-            }
+            const uint4 both = *reinterpret_cast<const uint4*>(st + (mt * 16 + h * 8 + gq) * PITCH + kKv4Scales);
+            ks[mt][h] = make_uint2(both.x, both.y);
+            vscale[mt][h] = make_uint2(both.z, both.w);
           }
           // sum over groups of scale * (-8 sum q), as a product of the scales and `shift`
           const uint32_t k0 = tq & 1 ? ks[mt][0].y : ks[mt][0].x;
           const uint32_t k1 = tq & 1 ? ks[mt][1].y : ks[mt][1].x;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_bf16(x[nt][mt], k0, k1, k0, k1, shift[nt][0], shift[nt][1]);
+          mma_bf16(x[mt], k0, k1, k0, k1, shift[0], shift[1]);
 #pragma unroll
           for (int gp = 0; gp < 2; ++gp) {
             uint32_t r[4];
@@ -545,38 +523,32 @@ __global__ void __launch_bounds__(Tile<NT, HB>::THREADS, Tile<NT, HB>::BLOCKS_PE
               const uint32_t lo = r[2 * gg], hi = r[2 * gg + 1], lo8 = lo >> 8, hi8 = hi >> 8;
               const uint32_t w0 = gp ? ks[mt][0].y : ks[mt][0].x, w1 = gp ? ks[mt][1].y : ks[mt][1].x;
               const float s0 = gg ? bf16_high(w0) : bf16_low(w0), s1 = gg ? bf16_high(w1) : bf16_low(w1);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                float acc[4];
-                mma_f16(acc, nib_even(lo), nib_even(hi), nib_odd(lo), nib_odd(hi), qb[nt][2 * gr][0],
-                        qb[nt][2 * gr][1]);
-                mma_f16(acc, nib_even(lo8), nib_even(hi8), nib_odd(lo8), nib_odd(hi8), qb[nt][2 * gr + 1][0],
-                        qb[nt][2 * gr + 1][1], acc);
-                float* xx = x[nt][mt];
-                xx[0] = fmaf(s0, acc[0], xx[0]); xx[1] = fmaf(s0, acc[1], xx[1]);
-                xx[2] = fmaf(s1, acc[2], xx[2]); xx[3] = fmaf(s1, acc[3], xx[3]);
-              }
+              float acc[4];
+              mma_f16(acc, nib_even(lo), nib_even(hi), nib_odd(lo), nib_odd(hi), qb[2 * gr][0],
+                      qb[2 * gr][1]);
+              mma_f16(acc, nib_even(lo8), nib_even(hi8), nib_odd(lo8), nib_odd(hi8), qb[2 * gr + 1][0],
+                      qb[2 * gr + 1][1], acc);
+              float* xx = x[mt];
+              xx[0] = fmaf(s0, acc[0], xx[0]); xx[1] = fmaf(s0, acc[1], xx[1]);
+              xx[2] = fmaf(s1, acc[2], xx[2]); xx[3] = fmaf(s1, acc[3], xx[3]);
             }
           }
         }
 
         // keys past the end get -inf; does a score or a V scale pass its bound?
         bool raise = __vmaxu2(big, scale_bound) != scale_bound;
-        float top[NT][2];
+        float top[2];
+        if (left < KEYS) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          if (left < KEYS) {
+          for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
+            for (int i = 0; i < 4; ++i)
+              if (mt * 16 + (i >> 1) * 8 + gq >= left) x[mt][i] = -INFINITY;
+        }
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (mt * 16 + (i >> 1) * 8 + gq >= left) x[nt][mt][i] = -INFINITY;
-          }
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            top[nt][j] = factor[nt][j] * fmaxf(fmax3(x[nt][0][j], x[nt][0][2 + j], x[nt][1][j]), x[nt][1][2 + j]);
-            raise = raise || top[nt][j] > limit[nt][j];
-          }
+        for (int j = 0; j < 2; ++j) {
+          top[j] = factor[j] * fmaxf(fmax3(x[0][j], x[0][2 + j], x[1][j]), x[1][2 + j]);
+          raise = raise || top[j] > limit[j];
         }
         if (__any_sync(0xffffffffu, raise)) {
           // E: |scale| < 2^E for all V scales so far (not below -90, so that p does not overflow
@@ -586,51 +558,42 @@ __global__ void __launch_bounds__(Tile<NT, HB>::THREADS, Tile<NT, HB>::BLOCKS_PE
           bound_E = E;
           scale_bound = ((uint32_t)((int)E + 126) << 7 | 0x7fu) * 0x10001u;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int j = 0; j < 2; ++j) {
+            float t = top[j];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              float t = top[nt][j];
+            for (int s = 4; s <= 16; s <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, s));
+            // what p was weighted with is `bias`, to the last bit: alpha and M go by it
+            const float now = fmaxf(limit[j] - kSlack, t);
+            const float to = now == -INFINITY ? kTop - E : kTop - E - now;
+            const float alpha = limit[j] == -INFINITY ? 0.f : ex2(to - bias[j].x);
+            limit[j] = now + kSlack;
+            bias[j] = make_float2(to, to);
+            l[j].x *= alpha;
+            l[j].y *= alpha;
 #pragma unroll
-              for (int s = 4; s <= 16; s <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, s));
-              // what p was weighted with is `bias`, to the last bit: alpha and M go by it
-              const float now = fmaxf(limit[nt][j] - kSlack, t);
-              const float to = now == -INFINITY ? kTop - E : kTop - E - now;
-              const float alpha = limit[nt][j] == -INFINITY ? 0.f : ex2(to - bias[nt][j].x);
-              limit[nt][j] = now + kSlack;
-              bias[nt][j] = make_float2(to, to);
-              l[nt][j].x *= alpha;
-              l[nt][j].y *= alpha;
+            for (int gr = 0; gr < 4; ++gr)
 #pragma unroll
-              for (int gr = 0; gr < 4; ++gr)
-#pragma unroll
-                for (int ti = 0; ti < 2; ++ti) {
-                  o[nt][gr][ti][j] *= alpha;
-                  o[nt][gr][ti][2 + j] *= alpha;
-                }
-            }
+              for (int ti = 0; ti < 2; ++ti) {
+                o[gr][ti][j] *= alpha;
+                o[gr][ti][2 + j] *= alpha;
+              }
+          }
         }
         // p of the keys (gq, gq + 8) of each 16, per column
-        float2 p[NT][2][2];
+        float2 p[2][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float2 y = fma2(make_float2(x[nt][mt][j], x[nt][mt][2 + j]),
-                                    make_float2(factor[nt][j], factor[nt][j]), bias[nt][j]);
-              p[nt][mt][j] = make_float2(ex2(y.x), ex2(y.y));
-              l[nt][j] = add2(l[nt][j], p[nt][mt][j]);
-            }
+          for (int j = 0; j < 2; ++j) {
+            const float2 y = fma2(make_float2(x[mt][j], x[mt][2 + j]),
+                                  make_float2(factor[j], factor[j]), bias[j]);
+            p[mt][j] = make_float2(ex2(y.x), ex2(y.y));
+            l[j] = add2(l[j], p[mt][j]);
+          }
 
         // O += (p scale)^T-fragments times V
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
-          if constexpr (NT == 2) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              vscale[mt][h] = lds_uint2(st32_scales + (mt * 16 + h * 8) * PITCH + 8);
-          }
 #pragma unroll
           for (int gp = 0; gp < 2; ++gp) {
             uint32_t r[4];
@@ -645,14 +608,11 @@ __global__ void __launch_bounds__(Tile<NT, HB>::THREADS, Tile<NT, HB>::BLOCKS_PE
                              a3 = code_odd(hi, magic);
               const uint32_t a4 = code_even(lo8, magic), a5 = code_odd(lo8, magic), a6 = code_even(hi8, magic),
                              a7 = code_odd(hi8, magic);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                const float2 p0 = mul2(p[nt][mt][0], s01), p1 = mul2(p[nt][mt][1], s01);
-                const uint32_t b0 = transpose8(pack_f16(p0.x, p1.x));
-                const uint32_t b1 = transpose8(pack_f16(p0.y, p1.y));
-                mma_f16(o[nt][gr][0], a0, a1, a2, a3, b0, b1, o[nt][gr][0]);
-                mma_f16(o[nt][gr][1], a4, a5, a6, a7, b0, b1, o[nt][gr][1]);
-              }
+              const float2 p0 = mul2(p[mt][0], s01), p1 = mul2(p[mt][1], s01);
+              const uint32_t b0 = transpose8(pack_f16(p0.x, p1.x));
+              const uint32_t b1 = transpose8(pack_f16(p0.y, p1.y));
+              mma_f16(o[gr][0], a0, a1, a2, a3, b0, b1, o[gr][0]);
+              mma_f16(o[gr][1], a4, a5, a6, a7, b0, b1, o[gr][1]);
             }
           }
         }
@@ -663,113 +623,104 @@ __global__ void __launch_bounds__(Tile<NT, HB>::THREADS, Tile<NT, HB>::BLOCKS_PE
     }
 
     // the sums of p over the warp, and M = -bias (-inf without a key) of the columns
-    float L[NT][2], M[NT][2];
+    float L[2], M[2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int j = 0; j < 2; ++j) {
+      L[j] = l[j].x + l[j].y;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        L[nt][j] = l[nt][j].x + l[nt][j].y;
-#pragma unroll
-        for (int s = 4; s <= 16; s <<= 1) L[nt][j] += __shfl_xor_sync(0xffffffffu, L[nt][j], s);
-        M[nt][j] = limit[nt][j] == -INFINITY ? -INFINITY : -bias[nt][j].x;
-      }
+      for (int s = 4; s <= 16; s <<= 1) L[j] += __shfl_xor_sync(0xffffffffu, L[j], s);
+      M[j] = limit[j] == -INFINITY ? -INFINITY : -bias[j].x;
+    }
     if constexpr (TL::PER_HEAD > 1) {
       // the head's other warps hand their states to its first
       constexpr int OTHERS = TL::PER_HEAD - 1;
       float* sm_o = reinterpret_cast<float*>(smem + STAGES * TL::STAGE_BYTES);  // [HB][OTHERS][ROWS][W]
       float* sm_ml = sm_o + OTHERS * HB * ROWS * W;                            // [HB][OTHERS][ROWS][2]
-      bar_consumers<TL::CW * 32>();  // the entry before has been joined
+      bar_consumers<CW * 32>();  // the entry before has been joined
       if (part) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int j = 0; j < 2; ++j) {
+          const int row = (hb * OTHERS + part - 1) * ROWS + 2 * tq + j;
+          if (gq == 0) *reinterpret_cast<float2*>(sm_ml + 2 * row) = make_float2(M[j], L[j]);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int row = (hb * OTHERS + part - 1) * ROWS + nt * 8 + 2 * tq + j;
-            if (gq == 0) *reinterpret_cast<float2*>(sm_ml + 2 * row) = make_float2(M[nt][j], L[nt][j]);
-#pragma unroll
-            for (int gr = 0; gr < 4; ++gr)
-              *reinterpret_cast<float4*>(sm_o + row * W + gr * 32 + gq * 4) =
-                  make_float4(o[nt][gr][0][j], o[nt][gr][0][2 + j], o[nt][gr][1][j], o[nt][gr][1][2 + j]);
-          }
+          for (int gr = 0; gr < 4; ++gr)
+            *reinterpret_cast<float4*>(sm_o + row * W + gr * 32 + gq * 4) =
+                make_float4(o[gr][0][j], o[gr][0][2 + j], o[gr][1][j], o[gr][1][2 + j]);
+        }
       }
-      bar_consumers<TL::CW * 32>();
+      bar_consumers<CW * 32>();
       if (part == 0) {
 #pragma unroll 1
         for (int w = 0; w < OTHERS; ++w)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int j = 0; j < 2; ++j) {
+            const int row = (hb * OTHERS + w) * ROWS + 2 * tq + j;
+            const float2 other = *reinterpret_cast<const float2*>(sm_ml + 2 * row);
+            // a state without keys, or with none above -inf, has M = -inf and nothing to add;
+            // only a NaN among its sums is passed on
+            const float top = fmaxf(M[j], other.x);
+            const float f0 = M[j] == -INFINITY ? 1.f : ex2(M[j] - top);
+            const float f1 = other.x == -INFINITY ? 1.f : ex2(other.x - top);
+            M[j] = top;
+            L[j] = fmaf(L[j], f0, other.y * f1);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const int row = (hb * OTHERS + w) * ROWS + nt * 8 + 2 * tq + j;
-              const float2 other = *reinterpret_cast<const float2*>(sm_ml + 2 * row);
-              // a state without keys, or with none above -inf, has M = -inf and nothing to add;
-              // only a NaN among its sums is passed on
-              const float top = fmaxf(M[nt][j], other.x);
-              const float f0 = M[nt][j] == -INFINITY ? 1.f : ex2(M[nt][j] - top);
-              const float f1 = other.x == -INFINITY ? 1.f : ex2(other.x - top);
-              M[nt][j] = top;
-              L[nt][j] = fmaf(L[nt][j], f0, other.y * f1);
-#pragma unroll
-              for (int gr = 0; gr < 4; ++gr) {
-                const float4 v = *reinterpret_cast<const float4*>(sm_o + row * W + gr * 32 + gq * 4);
-                o[nt][gr][0][j] = fmaf(o[nt][gr][0][j], f0, v.x * f1);
-                o[nt][gr][0][2 + j] = fmaf(o[nt][gr][0][2 + j], f0, v.y * f1);
-                o[nt][gr][1][j] = fmaf(o[nt][gr][1][j], f0, v.z * f1);
-                o[nt][gr][1][2 + j] = fmaf(o[nt][gr][1][2 + j], f0, v.w * f1);
-              }
+            for (int gr = 0; gr < 4; ++gr) {
+              const float4 v = *reinterpret_cast<const float4*>(sm_o + row * W + gr * 32 + gq * 4);
+              o[gr][0][j] = fmaf(o[gr][0][j], f0, v.x * f1);
+              o[gr][0][2 + j] = fmaf(o[gr][0][2 + j], f0, v.y * f1);
+              o[gr][1][j] = fmaf(o[gr][1][j], f0, v.z * f1);
+              o[gr][1][2 + j] = fmaf(o[gr][1][2 + j], f0, v.w * f1);
             }
+          }
       }
     }
     if (part == 0) {
       const bool whole = entry_begin >= range_begin && entry_end <= range_end;
+      const int row = 2 * tq;  // rows `row`, `row` + 1: the branches of one unit
+      if (whole) {
+        // a unit's 128 channels lie in the 8 lanes of a column pair, 16 to each
+        const bool mine = row0 + row < a.group;
+        const int u = a.v1 ? g : (g * a.group + row0 + row) >> 1;
+        const float lam = mine ? __ldg(a.lambda + u) : 0.f;
+        const float i0 = L[0] == 0.f ? 0.f : __fdiv_rn(1.f, L[0]);
+        const float i1 = L[1] == 0.f ? 0.f : __fdiv_rn(1.f, L[1]);
+        float y[4][4], ss = 0.f;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int row = nt * 8 + 2 * tq;  // rows `row`, `row` + 1: the branches of one unit
-        if (whole) {
-          // a unit's 128 channels lie in the 8 lanes of a column pair, 16 to each
-          const bool mine = row0 + row < a.group;
-          const int u = a.v1 ? g : (g * a.group + row0 + row) >> 1;
-          const float lam = mine ? __ldg(a.lambda + u) : 0.f;
-          const float i0 = L[nt][0] == 0.f ? 0.f : __fdiv_rn(1.f, L[nt][0]);
-          const float i1 = L[nt][1] == 0.f ? 0.f : __fdiv_rn(1.f, L[nt][1]);
-          float y[4][4], ss = 0.f;
+        for (int gr = 0; gr < 4; ++gr)
 #pragma unroll
-          for (int gr = 0; gr < 4; ++gr)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              // rounded alone, so that equal branches with lambda = 1 give exactly 0
-              const float o1 = __fmul_rn(o[nt][gr][i >> 1][2 * (i & 1)], i0);
-              const float o2 = __fmul_rn(o[nt][gr][i >> 1][2 * (i & 1) + 1], i1);
-              y[gr][i] = fmaf(-lam, o2, o1);
-              ss = fmaf(y[gr][i], y[gr][i], ss);
-            }
-          float f = 1.f;
-          if (a.apply_norm) {
-#pragma unroll
-            for (int s = 4; s <= 16; s <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, s);
-            f = rsqrtf(ss * (1.f / W) + a.eps) * (1.f - __ldg(a.lambda_init));
+          for (int i = 0; i < 4; ++i) {
+            // rounded alone, so that equal branches with lambda = 1 give exactly 0
+            const float o1 = __fmul_rn(o[gr][i >> 1][2 * (i & 1)], i0);
+            const float o2 = __fmul_rn(o[gr][i >> 1][2 * (i & 1) + 1], i1);
+            y[gr][i] = fmaf(-lam, o2, o1);
+            ss = fmaf(y[gr][i], y[gr][i], ss);
           }
-          const int64_t off = b * a.os[0] + (int64_t)u * a.os[1] + gq * 4;
+        float f = 1.f;
+        if (a.apply_norm) {
 #pragma unroll
-          for (int gr = 0; gr < 4; ++gr)
-            if (mine && in_bounds(off + gr * 32, 4, a.ext_out, a.cache.dev_status, a.cache.dbg_status))
-              *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + off + gr * 32) =
-                  make_uint2(pack_bf16(y[gr][0] * f, y[gr][1] * f), pack_bf16(y[gr][2] * f, y[gr][3] * f));
-        } else {
-          const int slot = entry_begin < range_begin ? 0 : 1;
+          for (int s = 4; s <= 16; s <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, s);
+          f = rsqrtf(ss * (1.f / W) + a.eps) * (1.f - __ldg(a.lambda_init));
+        }
+        const int64_t off = b * a.os[0] + (int64_t)u * a.os[1] + gq * 4;
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            if (row0 + row >= a.group) continue;
-            const int64_t rec = (((int64_t)blockIdx.x * 2 + slot) * HB + hb) * ROWS + row + j;
-            if (in_bounds(rec * W, W, a.ext_ws_o, a.cache.dev_status, a.cache.dbg_status)) {
+        for (int gr = 0; gr < 4; ++gr)
+          if (mine && in_bounds(off + gr * 32, 4, a.ext_out, a.cache.dev_status, a.cache.dbg_status))
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + off + gr * 32) =
+                make_uint2(pack_bf16(y[gr][0] * f, y[gr][1] * f), pack_bf16(y[gr][2] * f, y[gr][3] * f));
+      } else {
+        const int slot = entry_begin < range_begin ? 0 : 1;
 #pragma unroll
-              for (int gr = 0; gr < 4; ++gr)
-                *reinterpret_cast<float4*>(a.ws_o + rec * W + gr * 32 + gq * 4) =
-                    make_float4(o[nt][gr][0][j], o[nt][gr][0][2 + j], o[nt][gr][1][j], o[nt][gr][1][2 + j]);
-            }
-            if (gq == 0 && in_bounds(rec * 2, 2, a.ext_ws_ml, a.cache.dev_status, a.cache.dbg_status))
-              *reinterpret_cast<float2*>(a.ws_ml + rec * 2) = make_float2(M[nt][j], L[nt][j]);
+        for (int j = 0; j < 2; ++j) {
+          if (row0 + row >= a.group) continue;
+          const int64_t rec = (((int64_t)blockIdx.x * 2 + slot) * HB + hb) * ROWS + row + j;
+          if (in_bounds(rec * W, W, a.ext_ws_o, a.cache.dev_status, a.cache.dbg_status)) {
+#pragma unroll
+            for (int gr = 0; gr < 4; ++gr)
+              *reinterpret_cast<float4*>(a.ws_o + rec * W + gr * 32 + gq * 4) =
+                  make_float4(o[gr][0][j], o[gr][0][2 + j], o[gr][1][j], o[gr][1][2 + j]);
           }
+          if (gq == 0 && in_bounds(rec * 2, 2, a.ext_ws_ml, a.cache.dev_status, a.cache.dbg_status))
+            *reinterpret_cast<float2*>(a.ws_ml + rec * 2) = make_float2(M[j], L[j]);
         }
       }
     }
@@ -818,8 +769,8 @@ __global__ void __launch_bounds__(32 * SLICES) decode_kv4_combine_kernel(DecodeK
   const int u = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // the unit's head, row and head tile
   const int head = a.v1 ? u : 2 * u / a.group, row = 2 * u - head * a.group;
-  const int ck = KEYS * (compute_warps(a.nt) / a.heads), per = 8 * a.nt, tiles = (a.group + per - 1) / per;
-  const int HQ = a.H / a.heads * tiles, tile_h = head / a.heads * tiles + row / per;
+  const int ck = KEYS * (CW / a.heads), tiles = (a.group + ROWS - 1) / ROWS;
+  const int HQ = a.H / a.heads * tiles, tile_h = head / a.heads * tiles + row / ROWS;
   const uint32_t n = (kv4_len(a, b) + ck - 1) / ck;
   uint32_t T, begin;
   if (!a.kv_len) {
@@ -841,9 +792,9 @@ __global__ void __launch_bounds__(32 * SLICES) decode_kv4_combine_kernel(DecodeK
   if (n && i0 == i1) return;        // finished there
   // state s: slot 1 of range i0's block, then slot 0 of the ranges after it
   const int splits = n ? (int)(i1 - i0) + 1 : 0;
-  const int64_t step = 2LL * HQ * a.heads * per;
-  const int64_t rec0 = (((int64_t)i0 * HQ + tile_h) * 2 * a.heads + head % a.heads) * per + row % per;
-  auto record = [&](int s) { return rec0 + (s ? s * step : (int64_t)a.heads * per); };
+  const int64_t step = 2LL * HQ * a.heads * ROWS;
+  const int64_t rec0 = (((int64_t)i0 * HQ + tile_h) * 2 * a.heads + head % a.heads) * ROWS + row % ROWS;
+  auto record = [&](int s) { return rec0 + (s ? s * step : (int64_t)a.heads * ROWS); };
   const bool ok =
       !splits ||
       (in_bounds(record(splits - 1) * 2, 4, a.ext_ws_ml, a.cache.dev_status, a.cache.dbg_status) &&
@@ -929,24 +880,23 @@ static int kv4_heads(int H, int64_t head_stride) {
 // kMin. States are kept for two entries of every block.
 void decode_kv4_plan(DecodeKv4Args* a, int num_splits) {
   constexpr int64_t kMin = 2;
-  a->nt = a->group > 8 ? 2 : 1;
   a->heads = kv4_heads(a->H, a->cache.stride[2]);
-  const int64_t ck = KEYS * (compute_warps(a->nt) / a->heads);
-  const int64_t HQ = a->H / a->heads * ((a->group + 8 * a->nt - 1) / (8 * a->nt));
+  const int64_t ck = KEYS * (CW / a->heads);
+  const int64_t HQ = a->H / a->heads * ((a->group + ROWS - 1) / ROWS);
   a->chunks = (int64_t)a->B * ((a->cache.L + ck - 1) / ck);
-  int64_t groups = num_splits ? (int64_t)num_splits * a->B : 148 * (a->nt == 1 ? 3 : 1) / HQ;
+  int64_t groups = num_splits ? (int64_t)num_splits * a->B : 148 * kBlocksPerSm / HQ;
   const int64_t most = num_splits ? a->chunks : (a->chunks + kMin - 1) / kMin;
   if (groups > most) groups = most;
   if (groups > (1 << 16)) groups = 1 << 16;
   a->groups = groups < 1 ? 1 : (int)groups;
   a->blocks = a->groups * HQ;
-  a->states = a->blocks * 2 * a->heads * 8 * a->nt;
+  a->states = a->blocks * 2 * a->heads * ROWS;
 }
 
 // HB = 1: {144 bytes, heads, rows, entries or pages}, boxes of one head's records; else
 // {bytes of a token's heads, 1, rows, entries or pages}, boxes of HB heads' records and 16
 // bytes (zeros behind the last head). 4-byte elements. False where TMA does not take the strides.
-template <int NT, int HB>
+template <int HB>
 static bool kv4_map(CUtensorMap* m, const Kv4Cache& c, int H, int rows, int outer, int box) {
   auto fn = encode_fn();
   if (!fn || rows < 1) return false;
@@ -959,28 +909,28 @@ static bool kv4_map(CUtensorMap* m, const Kv4Cache& c, int H, int rows, int oute
   if (HB != 1) hs = (int64_t)inner * 4;
   const cuuint64_t dims[4] = {(cuuint64_t)inner, (cuuint64_t)(HB == 1 ? H : 1), (cuuint64_t)rows, (cuuint64_t)outer};
   const cuuint64_t strides[3] = {(cuuint64_t)hs, (cuuint64_t)ts, (cuuint64_t)os};
-  const cuuint32_t boxes[4] = {(cuuint32_t)Tile<NT, HB>::PITCH / 4, 1, (cuuint32_t)box, 1};
+  const cuuint32_t boxes[4] = {(cuuint32_t)Tile<HB>::PITCH / 4, 1, (cuuint32_t)box, 1};
   const cuuint32_t steps[4] = {1, 1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, c.base, dims, strides, boxes, steps,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NT, int HB>
+template <int HB>
 static cudaError_t launch_split(const DecodeKv4Args& a, cudaStream_t stream) {
-  using TL = Tile<NT, HB>;
+  using TL = Tile<HB>;
   const bool paged = a.cache.block_table != nullptr;
   const int page = 1 << a.cache.page_shift;
   CUtensorMap map;
   memset(&map, 0, sizeof(map));
   Kv4Load how = kRows;
-  if (!paged && kv4_map<NT, HB>(&map, a.cache, a.H, a.cache.L, a.B, TL::CK)) how = kTma;
+  if (!paged && kv4_map<HB>(&map, a.cache, a.H, a.cache.L, a.B, TL::CK)) how = kTma;
   if (paged && page >= 8 &&
-      kv4_map<NT, HB>(&map, a.cache, a.H, page, a.cache.num_pages, page < TL::CK ? page : TL::CK))
+      kv4_map<HB>(&map, a.cache, a.H, page, a.cache.num_pages, page < TL::CK ? page : TL::CK))
     how = kTmaPaged;
-  void (*const fns[3])(CUtensorMap, DecodeKv4Args) = {decode_kv4_split_kernel<NT, HB, kTma>,
-                                                      decode_kv4_split_kernel<NT, HB, kTmaPaged>,
-                                                      decode_kv4_split_kernel<NT, HB, kRows>};
+  void (*const fns[3])(CUtensorMap, DecodeKv4Args) = {decode_kv4_split_kernel<HB, kTma>,
+                                                      decode_kv4_split_kernel<HB, kTmaPaged>,
+                                                      decode_kv4_split_kernel<HB, kRows>};
   void (*const fn)(CUtensorMap, DecodeKv4Args) = fns[how];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -991,16 +941,13 @@ static cudaError_t launch_split(const DecodeKv4Args& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_set[how][dev] = true;
   }
-  fn<<<(unsigned)a.blocks, TL::THREADS, TL::SMEM_BYTES, stream>>>(map, a);
+  fn<<<(unsigned)a.blocks, THREADS, TL::SMEM_BYTES, stream>>>(map, a);
   return cudaGetLastError();
 }
 
 cudaError_t launch_decode_kv4(const DecodeKv4Args& a, cudaStream_t stream) {
-  cudaError_t e;
-  if (a.nt == 1)
-    e = a.heads == 4 ? launch_split<1, 4>(a, stream) : (a.heads == 2 ? launch_split<1, 2>(a, stream) : launch_split<1, 1>(a, stream));
-  else
-    e = a.heads == 4 ? launch_split<2, 4>(a, stream) : (a.heads == 2 ? launch_split<2, 2>(a, stream) : launch_split<2, 1>(a, stream));
+  const cudaError_t e =
+      a.heads == 4 ? launch_split<4>(a, stream) : (a.heads == 2 ? launch_split<2>(a, stream) : launch_split<1>(a, stream));
   if (e != cudaSuccess) return e;
   // launched while the last blocks still run; the kernel waits for them itself
   cudaLaunchAttribute attr;

@@ -171,7 +171,7 @@ struct DecodeKv4Args {
   int B, Hq, H;           // V1: Hq = H heads of two branches; V2: Hq query heads over H
   int v1;
   int group;              // query rows of a KV head: V1 2 (its branches), V2 Hq / H
-  int nt, heads, groups;  // query tiles of 8, KV heads of a block, groups (decode_kv4_plan)
+  int heads, groups;      // KV heads of a block, groups of blocks (decode_kv4_plan)
   int64_t chunks;         // of full-length entries
   int64_t blocks, states; // of the launch; rows of the workspace
   int64_t qs[2], os[2];
@@ -182,14 +182,14 @@ struct DecodeKv4Args {
   int apply_norm;
   float eps;
   void* out;
-  float* ws_o;            // [blocks, 2 slots, heads, 8 nt, 128]
-  float* ws_ml;           // [blocks, 2 slots, heads, 8 nt, 2]
+  float* ws_o;            // [blocks, 2 slots, heads, 8 rows, 128]
+  float* ws_ml;           // [blocks, 2 slots, heads, 8 rows, 2]
   int64_t ext_q, ext_out, ext_ws_o, ext_ws_ml;
 };
 
 cudaError_t launch_kv4_write(const Kv4RowsArgs& a, cudaStream_t stream);
 cudaError_t launch_kv4_read(const Kv4RowsArgs& a, cudaStream_t stream);
-// fills nt to states from the other fields
+// fills heads to states from the other fields
 void decode_kv4_plan(DecodeKv4Args* a, int num_splits);
 cudaError_t launch_decode_kv4(const DecodeKv4Args& a, cudaStream_t stream);
 

@@ -528,8 +528,8 @@ int diffattn_kv4_read(const diffattn_kv4_rows* p, const diffattn_paged_kv* pk, c
 /*
  * diffattn_fwd_decode_kv4 -- diffattn_fwd_decode (p->variant = DIFFATTN_V2) or
  * diffattn_fwd_decode_v1 (DIFFATTN_V1) over a cache held in 4 bits: the attention over the
- * values diffattn_kv4_read gives in f32, reading each record once for all query heads of a KV
- * head (of up to 16).
+ * values diffattn_kv4_read gives in f32, reading each record once for up to 8 query heads of a
+ * KV head.
  *   p           : as for those calls, with p->kv_strides the cache's BYTE strides (ignored
  *                 when paged); V2: d = 128 and any even Hq / Hkv; V1: d = 64; max_kv_len at
  *                 most 2^30; num_splits the parts the keys of an entry are cut into on
@@ -542,7 +542,8 @@ int diffattn_kv4_read(const diffattn_kv4_rows* p, const diffattn_paged_kv* pk, c
  *   lambda_init, apply_norm, norm_eps : V1 as for diffattn_fwd_decode_v1; V2: apply_norm = 0
  *   workspace   : >= diffattn_decode_kv4_workspace_size(p, pk) bytes, 256-byte aligned; calls
  *                 sharing a workspace must not overlap in time. Its size does not grow with
- *                 the lengths (at most 20 MB with num_splits = 0)
+ *                 the lengths (at most 15 MB with num_splits = 0, up to 444
+ *                 head tiles)
  * Arithmetic: q and the codes are exact MMA operands (q after a power-of-two scaling per row;
  * elements under 2^-31 of a row's largest lose bits, and rows with elements past 2^117
  * overflow), scales, sums and softmax statistics in fp32, probability times V scale rounded
