@@ -865,16 +865,15 @@ def diffattn_fwd_decode_kv4(q, cache, lam, kv_len=None, lambda_init=None, out=No
     [B,L,H,144], or a pool [P,page,H,144] with block_table int32 [B,pages]. V2: q [B,Hq,128] ->
     out [B,Hq/2,128]. V1: q [B,H,2,64] -> out [B,H,128] (norm and scale when apply_norm, default
     on). max_kv_len defaults to the positions the cache or the block table has room for."""
-    import torch
     lib = load_library()
     p, pk, need, shape, v1, _ = _kv4_plan(_kv4_decode_plan, (int(num_splits), _int(max_kv_len)), q, cache, lam, kv_len,
                                           lambda_init, out, block_table, dev_status)
     device = cache.device
     with _Kv4Scope(device, stream) as on:
         if out is None:
-            out = torch.empty(shape, dtype=torch.bfloat16, device=device)
+            out = q.new_empty(shape)
         if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+            workspace = cache.new_empty(need)
             ws_bytes = need
         else:
             if workspace.device != device or not workspace.is_contiguous():

@@ -221,19 +221,37 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm)
   fence_barrier_init();
   cudaTriggerProgrammaticLaunchCompletion();
 
-  // this block's range and where it begins
-  uint32_t T = 0;
+  // this block's range and where it begins: chunks of the entries before each (`scan`, of THREADS
+  // entries at a time)
+  uint32_t T = 0, n = 0, scan = 0;
+  auto scan_entries = [&](int b0, uint32_t before) {  // returns the chunks up to their end
+    n = b0 + tid < a.B ? (kv4_len(a, b0 + tid) + CK - 1) / CK : 0;
+    scan = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t up = __shfl_up_sync(0xffffffffu, scan, o);
+      if (lane >= o) scan += up;
+    }
+    if (lane == 31) sums[warp] = scan;
+    __syncthreads();
+    scan += before;
+    for (int w = 0; w < WARPS; ++w) {
+      if (w < warp) scan += sums[w];
+      before += sums[w];
+    }
+    __syncthreads();
+    return before;
+  };
   if (!a.kv_len) {
-    T = (uint32_t)a.B * ((a.cache.L + CK - 1) / CK);
+    n = (a.cache.L + CK - 1) / CK;
+    T = (uint32_t)a.B * n;
   } else {
-    for (int b0 = 0; b0 < a.B; b0 += THREADS)
-      T += block_sum(b0 + tid < a.B ? (kv4_len(a, b0 + tid) + CK - 1) / CK : 0, sums, WARPS);
+    for (int b0 = 0; b0 < a.B; b0 += THREADS) T = scan_entries(b0, T);
   }
   const Kv4Cuts cuts(T, a.groups);
   const uint32_t range_begin = cuts.begin(group), range_end = cuts.begin(group + 1);
   if (group >= min((uint32_t)a.groups, T)) return;
   if (!a.kv_len) {
-    const uint32_t n = (a.cache.L + CK - 1) / CK;
     if (tid == 0) {
       first[0] = range_begin / n;
       first[1] = range_begin / n * n;
@@ -241,21 +259,7 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm)
   } else {
     uint32_t before = 0;
     for (int b0 = 0; b0 < a.B && before <= range_begin; b0 += THREADS) {
-      const uint32_t n = b0 + tid < a.B ? (kv4_len(a, b0 + tid) + CK - 1) / CK : 0;
-      uint32_t scan = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t up = __shfl_up_sync(0xffffffffu, scan, o);
-        if (lane >= o) scan += up;
-      }
-      __syncthreads();
-      if (lane == 31) sums[warp] = scan;
-      __syncthreads();
-      scan += before;
-      for (int w = 0; w < WARPS; ++w) {
-        if (w < warp) scan += sums[w];
-        before += sums[w];
-      }
+      before = a.B <= THREADS ? T : scan_entries(b0, before);
       if (scan - n <= range_begin && range_begin < scan) {
         first[0] = b0 + tid;
         first[1] = scan - n;
@@ -758,15 +762,18 @@ __device__ __forceinline__ void store_unit(const DecodeKv4Args& a, int b, int u,
 // took 52 us with a thread to a channel walking them all.) SLICES = 16 for few entries with
 // many states each, 4 for many with few: 222 states of one entry took 15 us instead of 32,
 // 10 states each of 24 entries 18 us instead of 29.
-template <int SLICES>
+// Few entries also split a unit's channels over W / CH blocks, where no norm runs over them.
+template <int SLICES, int CH>
 __global__ void __launch_bounds__(32 * SLICES) decode_kv4_combine_kernel(DecodeKv4Args a) {
   constexpr int JOIN = 32 * SLICES;  // states whose weights are held at a time
+  constexpr int LANES = CH / 4, AT_ONCE = 32 / LANES;  // lanes of a state, states of a warp at once
   __shared__ float weight[2][JOIN];
-  __shared__ float4 part[SLICES][2][W / 4];
+  __shared__ float4 part[SLICES * AT_ONCE][2][LANES];
   __shared__ float red[2][SLICES];
   __shared__ uint32_t sums[SLICES];
   constexpr int THREADS = 32 * SLICES;
   const int u = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int c0 = blockIdx.z * CH;
   // the unit's head, row and head tile
   const int head = a.v1 ? u : 2 * u / a.group, row = 2 * u - head * a.group;
   const int ck = KEYS * (CW / a.heads), tiles = (a.group + ROWS - 1) / ROWS;
@@ -836,8 +843,8 @@ __global__ void __launch_bounds__(32 * SLICES) decode_kv4_combine_kernel(DecodeK
     }
     __syncthreads();
 #pragma unroll 4
-    for (int s = warp; s < held; s += SLICES) {
-      const float4* po = reinterpret_cast<const float4*>(a.ws_o + record(s0 + s) * W) + lane;
+    for (int s = warp * AT_ONCE + lane / LANES; s < held; s += SLICES * AT_ONCE) {
+      const float4* po = reinterpret_cast<const float4*>(a.ws_o + record(s0 + s) * W + c0) + lane % LANES;
       const float4 v0 = po[0], v1 = po[W / 4];
       const float f0 = weight[0][s], f1 = weight[1][s];
       O[0] = make_float4(fmaf(v0.x, f0, O[0].x), fmaf(v0.y, f0, O[0].y), fmaf(v0.z, f0, O[0].z), fmaf(v0.w, f0, O[0].w));
@@ -849,22 +856,21 @@ __global__ void __launch_bounds__(32 * SLICES) decode_kv4_combine_kernel(DecodeK
   for (int e = 0; e < 2; ++e) {
     L[e] = warp_sum(L[e]);
     if (lane == 0) red[e][warp] = L[e];
-    part[warp][e][lane] = O[e];
+    part[warp * AT_ONCE + lane / LANES][e][lane % LANES] = O[e];
   }
   __syncthreads();
-  const int c = tid % W;  // the first W threads finish, a channel each
+  const int c = tid % CH;  // the first CH threads finish, a channel each
   float res[2];
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     float l = 0.f, o = 0.f;
-    for (int w = 0; w < SLICES; ++w) {
-      l += red[e][w];
-      o += reinterpret_cast<const float*>(part[w][e])[c];
-    }
+    for (int w = 0; w < SLICES; ++w) l += red[e][w];
+#pragma unroll 8
+    for (int w = 0; w < SLICES * AT_ONCE; ++w) o += reinterpret_cast<const float*>(part[w][e])[c];
     res[e] = l == 0.f ? 0.f : o / l;
   }
   __syncthreads();
-  store_unit(a, b, u, c, tid < W, res[0], res[1], red[0]);
+  store_unit(a, b, u, c0 + c, tid < CH, res[0], res[1], red[0]);
 }
 
 // Heads of a block: neighbours read together (one run of 144 HB bytes per token) when the
@@ -956,12 +962,14 @@ cudaError_t launch_decode_kv4(const DecodeKv4Args& a, cudaStream_t stream) {
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = dim3(a.H * a.group / 2, a.B);
-  const bool many = a.groups > 64 * (int64_t)a.B;
+  const bool many = a.groups > 64 * (int64_t)a.B, spread = many && !a.apply_norm;
   cfg.blockDim = dim3(many ? 512 : 128);
+  if (spread) cfg.gridDim.z = W / 32;
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, many ? decode_kv4_combine_kernel<16> : decode_kv4_combine_kernel<4>, a);
+  return cudaLaunchKernelEx(&cfg, spread ? decode_kv4_combine_kernel<16, 32>
+                                         : (many ? decode_kv4_combine_kernel<16, W> : decode_kv4_combine_kernel<4, W>), a);
 }
 
 }  // namespace diffattn
