@@ -28,9 +28,16 @@
 //     added; for V the probability is multiplied by the scale in fp32 and rounded to fp16
 //     once (2^-12 relative; bf16's 2^-9 would be amplified by the subtraction and V1's norm).
 //     fp16's range is kept by the running maximum: M bounds x + E, E the exponent of the
-//     chunk's largest V scale, so products lie under 2^(kTop + kSlack) = 2^15, and M is
-//     raised only when the bound would be passed. Products under 2^-22 of the largest
-//     probability times the largest scale become subnormal and lose bits.
+//     largest V scale so far, so products lie under 2^(kTop + kSlack), and M is raised only
+//     when the bound would be passed. Products under 2^-22 of the largest probability times
+//     the largest scale become subnormal and lose bits.
+//   * The branches' rounding errors do not cancel in O_1 / l_1 - lambda O_2 / l_2, while the
+//     values may: with lambda near 1 and flat scores (V1's norm then scales the rest up) the
+//     output was 0.0027 off in relative terms where its bf16 rounding alone makes 0.0016. So
+//     the operand of branch 1 is p_1 - c p_2, formed in fp32, with c near lambda l_1 / l_2 and
+//     at most 1: D = O_1 - c O_2 carries errors of its own size only, those of O_2 cancel, and
+//     O_1 = D + c O_2 is put together in fp32 when the warp is done. Both branches of a unit
+//     are neighbouring columns of one lane, so this costs two instructions a chunk.
 //   * q is taken times a power of two per row so that its largest element is in [2^14, 2^15);
 //     fp16 then holds every element above 2^-31 of the largest exactly.
 #include <cuda_fp16.h>
@@ -46,7 +53,7 @@ namespace {
 constexpr int W = kKv4Width;
 constexpr int KEYS = 32;      // keys that a warp takes of a chunk
 constexpr float kTop = 8.f;   // p * scale <= 2^kTop when the maximum is raised ...
-constexpr float kSlack = 7.f; // ... and <= 2^(kTop + kSlack) before
+constexpr float kSlack = 6.f; // ... and <= 2^(kTop + kSlack) before: |(p_1 - c p_2) scale| <= 2^15
 
 // A block has CW warps that compute and one that issues the copies; three blocks to an SM.
 constexpr int CW = 4;
@@ -463,7 +470,11 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm)
     float2 bias[2], l[2];
     float bound_E = -90.f;
     uint32_t scale_bound = 0;  // bf16 bits that no V scale so far passes, twice
-    // [group][tile]: channels 32 g + 4 gq + 2 tile + {0, 1}
+    const bool is_unit = row0 + 2 * tq < a.group;  // columns 2 tq, 2 tq + 1: the branches of unit u
+    const int u = a.v1 ? g : (g * a.group + row0 + 2 * tq) >> 1;
+    const float lam = is_unit ? __ldg(a.lambda + u) : 0.f;
+    float c = 0.f;  // column 2 tq accumulates p_1 - c p_2
+    // [group][tile]: channels 32 g + 4 gq + 2 tile + {0, 1}; elements 0, 2 column 2 tq, 1, 3 the next
     float o[4][2][4];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -479,7 +490,7 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm)
         for (int i = 0; i < 4; ++i) o[gr][ti][i] = 0.f;
 
     int left = kv_len - (int)(at - entry_begin) * CK - part * KEYS;  // keys from this warp's first on
-    for (uint32_t c = at; c < stop; ++c, left -= CK) {
+    for (uint32_t chunk = at; chunk < stop; ++chunk, left -= CK) {
       if (ok) {
         ok = mbar_wait(&full[stage], parity, &abort_flag);
         ok = __all_sync(0xffffffffu, ok);
@@ -561,6 +572,7 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm)
           const float E = fmaxf((float)((int)(most >> 7) - 126), bound_E);
           bound_E = E;
           scale_bound = ((uint32_t)((int)E + 126) << 7 | 0x7fu) * 0x10001u;
+          float alpha[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             float t = top[j];
@@ -569,19 +581,26 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm)
             // what p was weighted with is `bias`, to the last bit: alpha and M go by it
             const float now = fmaxf(limit[j] - kSlack, t);
             const float to = now == -INFINITY ? kTop - E : kTop - E - now;
-            const float alpha = limit[j] == -INFINITY ? 0.f : ex2(to - bias[j].x);
+            alpha[j] = limit[j] == -INFINITY ? 0.f : ex2(to - bias[j].x);
             limit[j] = now + kSlack;
             bias[j] = make_float2(to, to);
-            l[j].x *= alpha;
-            l[j].y *= alpha;
-#pragma unroll
-            for (int gr = 0; gr < 4; ++gr)
-#pragma unroll
-              for (int ti = 0; ti < 2; ++ti) {
-                o[gr][ti][j] *= alpha;
-                o[gr][ti][2 + j] *= alpha;
-              }
+            l[j].x *= alpha[j];
+            l[j].y *= alpha[j];
           }
+          // D <- alpha_1 (D + c O_2) - c' alpha_2 O_2, O_2 <- alpha_2 O_2, c' for the new maxima
+          const bool both = alpha[0] > 0.f && alpha[1] > 0.f;
+          const float next = both ? fminf(fmaxf(__fmul_rn(c, __fdiv_rn(alpha[0], alpha[1])), -1.f), 1.f) : 0.f;
+          const float back = __fmul_rn(alpha[0], c) - __fmul_rn(next, alpha[1]);
+          c = next;
+#pragma unroll
+          for (int gr = 0; gr < 4; ++gr)
+#pragma unroll
+            for (int ti = 0; ti < 2; ++ti)
+#pragma unroll
+              for (int i = 0; i < 4; i += 2) {
+                o[gr][ti][i] = fmaf(back, o[gr][ti][i + 1], __fmul_rn(alpha[0], o[gr][ti][i]));
+                o[gr][ti][i + 1] *= alpha[1];
+              }
         }
         // p of the keys (gq, gq + 8) of each 16, per column
         float2 p[2][2];
@@ -594,6 +613,35 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm)
             p[mt][j] = make_float2(ex2(y.x), ex2(y.y));
             l[j] = add2(l[j], p[mt][j]);
           }
+        // c by the sums so far at chunks 1, 2, 4, ..., and whenever it has come to be more than 4
+        // times lambda l_1 / l_2 in any lane's share of the keys (and so, at most, in all): past
+        // that its error would outgrow the one it saves. Lanes that disagree, as they do under
+        // peaked scores, make it small.
+        const uint32_t nth = chunk - at + 1;
+        const float mine1 = l[0].x + l[0].y, mine2 = l[1].x + l[1].y;
+        const bool large = fabsf(c) * mine2 > 4.f * fabsf(lam) * mine1;
+        if (__any_sync(0xffffffffu, large) || (nth & (nth - 1)) == 0) {
+          float s1 = mine1, s2 = mine2, least = mine2 > 0.f ? 4.f * __fdiv_rn(mine1, mine2) : INFINITY;
+#pragma unroll
+          for (int s = 4; s <= 16; s <<= 1) {
+            s1 += __shfl_xor_sync(0xffffffffu, s1, s);
+            s2 += __shfl_xor_sync(0xffffffffu, s2, s);
+            least = fminf(least, __shfl_xor_sync(0xffffffffu, least, s));
+          }
+          const float ratio = s2 > 0.f ? fminf(__fdiv_rn(s1, s2), least) : 0.f;
+          const float next = fminf(fmaxf(__fmul_rn(lam, ratio), -1.f), 1.f);
+          const float back = c - next;
+          c = next;
+#pragma unroll
+          for (int gr = 0; gr < 4; ++gr)
+#pragma unroll
+            for (int ti = 0; ti < 2; ++ti)
+#pragma unroll
+              for (int i = 0; i < 4; i += 2) o[gr][ti][i] = fmaf(back, o[gr][ti][i + 1], o[gr][ti][i]);
+        }
+        // the operand of column 2 tq, see c
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) p[mt][0] = fma2(p[mt][1], make_float2(-c, -c), p[mt][0]);
 
         // O += (p scale)^T-fragments times V
 #pragma unroll
@@ -625,6 +673,13 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm)
       if (lane == 0) mbar_arrive(&empty[stage]);
       advance();
     }
+    // O_1 from D
+#pragma unroll
+    for (int gr = 0; gr < 4; ++gr)
+#pragma unroll
+      for (int ti = 0; ti < 2; ++ti)
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) o[gr][ti][i] = fmaf(c, o[gr][ti][i + 1], o[gr][ti][i]);
 
     // the sums of p over the warp, and M = -bias (-inf without a key) of the columns
     float L[2], M[2];
@@ -680,12 +735,8 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm)
     }
     if (part == 0) {
       const bool whole = entry_begin >= range_begin && entry_end <= range_end;
-      const int row = 2 * tq;  // rows `row`, `row` + 1: the branches of one unit
       if (whole) {
         // a unit's 128 channels lie in the 8 lanes of a column pair, 16 to each
-        const bool mine = row0 + row < a.group;
-        const int u = a.v1 ? g : (g * a.group + row0 + row) >> 1;
-        const float lam = mine ? __ldg(a.lambda + u) : 0.f;
         const float i0 = L[0] == 0.f ? 0.f : __fdiv_rn(1.f, L[0]);
         const float i1 = L[1] == 0.f ? 0.f : __fdiv_rn(1.f, L[1]);
         float y[4][4], ss = 0.f;
@@ -708,15 +759,15 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm)
         const int64_t off = b * a.os[0] + (int64_t)u * a.os[1] + gq * 4;
 #pragma unroll
         for (int gr = 0; gr < 4; ++gr)
-          if (mine && in_bounds(off + gr * 32, 4, a.ext_out, a.cache.dev_status, a.cache.dbg_status))
+          if (is_unit && in_bounds(off + gr * 32, 4, a.ext_out, a.cache.dev_status, a.cache.dbg_status))
             *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + off + gr * 32) =
                 make_uint2(pack_bf16(y[gr][0] * f, y[gr][1] * f), pack_bf16(y[gr][2] * f, y[gr][3] * f));
       } else {
         const int slot = entry_begin < range_begin ? 0 : 1;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          if (row0 + row >= a.group) continue;
-          const int64_t rec = (((int64_t)blockIdx.x * 2 + slot) * HB + hb) * ROWS + row + j;
+          if (!is_unit) continue;
+          const int64_t rec = (((int64_t)blockIdx.x * 2 + slot) * HB + hb) * ROWS + 2 * tq + j;
           if (in_bounds(rec * W, W, a.ext_ws_o, a.cache.dev_status, a.cache.dbg_status)) {
 #pragma unroll
             for (int gr = 0; gr < 4; ++gr)

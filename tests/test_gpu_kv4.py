@@ -398,6 +398,35 @@ def test_decode_equal_branches_cancel_exactly():
     assert (out == 0).all()
 
 
+@pytest.mark.parametrize("L,splits", [(20, 1), (700, 1), (6000, 0)])
+def test_decode_flat_scores_and_lambda_near_one(L, splits):
+    """Nearly equal branches and lambda near 1, where V1's norm scales up what the difference
+    leaves. Branch 1's operand is p_1 - c p_2, so fp16's 2^-11 is allowed on the difference of
+    the weights only, and on a tenth of branch 2's for c's own distance from lambda l_1 / l_2
+    (scores of standard deviation 0.12 keep l_1 / l_2 within that over any share of the keys);
+    fp32 scores and sums take 2^-16 of both, and the result is rounded to bf16."""
+    H = 4
+    c, rec, q, qx, lam = _decode_case(1, 2, H, H, L, [L, L], seed=L, qscale=0.125, kscale=0.125, vscale=0.125)
+    lam = np.array([1.0, 0.97, 1.03, 0.9], np.float32)
+    li = np.float32(0.7778701)
+    out = da.diffattn_fwd_decode_kv4(q, c.t, torch.from_numpy(lam).cuda(), lambda_init=torch.full((1,), float(li), device="cuda"),
+                                     num_splits=splits).double().cpu().numpy()
+    for b in range(2):
+        for h in range(H):
+            k, v = plain.values(rec[b, :, h])
+            w = []
+            for e in range(2):
+                p = np.exp(k[:, 64 * e:64 * e + 64] @ qx[b, h, e] / 8)
+                w.append(p / p.sum())
+            y = (w[0] - lam[h] * w[1]) @ v
+            dy = 2.0 ** -11 * (np.abs(w[0] - lam[h] * w[1]) + 0.1 * lam[h] * w[1]) @ np.abs(v)
+            dy += 2.0 ** -16 * (w[0] + lam[h] * w[1]) @ np.abs(v)
+            r = np.sqrt((y * y).mean() + 1e-5)
+            dy = (dy + np.abs(y) * np.sqrt((dy * dy).mean()) / r) / r * (1 - li)
+            y = y / r * (1 - li)
+            assert (np.abs(out[b, h] - y) <= dy + 2.0 ** -8 * (np.abs(y) + dy)).all(), (b, h)
+
+
 def test_decode_nan_stays_where_it_is():
     lens = [200, 200, 200]
     c, rec, q, qx, lam = _decode_case(2, 3, 16, 2, 200, lens, seed=13)
