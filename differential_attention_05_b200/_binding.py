@@ -621,6 +621,8 @@ def _kv4_tensor(fn, name, t, dtype, device, shape=None, dense=True):
         _kv4_fail(fn, f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
     if dense and not t.is_contiguous():
         _kv4_fail(fn, f"{name} must be contiguous")
+    if name in ("dev_status", "lambda_init") and t.numel() < 1:
+        _kv4_fail(fn, f"{name} is empty")
 
 
 def _kv4_cache(fn, cache, block_table, max_kv_len, batch):

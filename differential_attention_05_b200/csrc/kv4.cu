@@ -8,7 +8,7 @@
 // would near the subnormals); a group with a NaN or an infinity gets a NaN scale, so that
 // its values read back as NaN.
 //
-// The kernels write n without a division for each element: with r = 1 / scale rounded,
+// The kernels write n without a division for each element: with r = 1 / scale to 2^-23,
 // x r is within 2^-22 of x / scale in relative terms, and adding and taking away 1.5 * 2^11
 // rounds it to a multiple of 2^-12; a tie comes out exactly, and anything else stays on its
 // side of one (x / scale is at most 8 in magnitude and at least 2^-10 from a tie it does not
@@ -80,17 +80,22 @@ struct Kv4Lane {
   }
 };
 
+// 1 / x to 2^-23 in relative terms
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // 8 codes and the bf16 bits of the scale of 8 channels (bf16 pairs w), which with those of
 // the three lanes beside it make a group
 __device__ __forceinline__ uint32_t kv4_encode(const uint32_t (&w)[4], uint32_t& scale_bits) {
   // The largest magnitude among the group's positive values (low half) and among its
   // negative ones (high half), on bf16 bits: as signed 16-bit integers the largest is the
   // largest positive value, as unsigned ones the largest negative one.
-  const uint32_t up = __vmaxs2(__vmaxs2(w[0], w[1]), __vmaxs2(w[2], w[3]));
-  const uint32_t down = __vmaxu2(__vmaxu2(w[0], w[1]), __vmaxu2(w[2], w[3]));
-  const int pos = max(max((int)(int16_t)up, (int)up >> 16), 0);
-  const int neg = max((int)max(down & 0xffffu, down >> 16) - 0x8000, 0);
-  uint32_t most = (uint32_t)pos | (uint32_t)neg << 16;
+  const uint32_t up = __vmaxs2(__vmaxs2(__vmaxs2(w[0], w[1]), __vmaxs2(w[2], w[3])), 0u);
+  const uint32_t down = __vmaxu2(__vmaxu2(__vmaxu2(w[0], w[1]), __vmaxu2(w[2], w[3])), 0x80008000u) ^ 0x80008000u;
+  uint32_t most = __vmaxu2(__byte_perm(up, down, 0x5410), __byte_perm(up, down, 0x7632));
   most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, 1));
   most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, 2));
   const uint32_t p16 = most & 0xffffu, n16 = most >> 16, size = max(p16, n16);
@@ -101,7 +106,7 @@ __device__ __forceinline__ uint32_t kv4_encode(const uint32_t (&w)[4], uint32_t&
   // kFine in [2^11, 2^12): units of 2^-12; adding kWhole - kFine, exact up to its own
   // rounding, then gives the integer on top of kWhole = 1.5 * 2^23
   constexpr float kFine = 1.5f * 2048.f, kWhole = 12582912.f;
-  const float inv = __frcp_rn(scale);
+  const float inv = rcp_approx(scale);
   float2 k[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -222,8 +227,17 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_read_kernel(Kv4RowsArgs a) {
   }
 #pragma unroll
   for (int s = 0; s < STEPS; ++s) {
-    const int r = 2 * s + sub;
-    if (at.row(r) >= e.n) break;
+    const int r = 2 * s + sub, odd = at.c & 1;
+    if constexpr (F32) {
+      // a pair of lanes swaps halves of its 16 channels, so that a store of 16 bytes per lane
+      // fills whole 32-byte sectors: channels 4 odd .. and 8 + 4 odd .. of the pair's
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, codes[s][q], 1);
+        codes[s][q] = odd ? __byte_perm(other, codes[s][q], 0x7632) : __byte_perm(codes[s][q], other, 0x5410);
+      }
+    }
+    if (at.row(r) >= e.n) continue;
     const int64_t off = at.channels(r);
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
@@ -232,11 +246,11 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_read_kernel(Kv4RowsArgs a) {
       const __nv_bfloat162 n[4] = {kv4_pair<0>(w), kv4_pair<1>(w), kv4_pair<2>(w), kv4_pair<3>(w)};
       if constexpr (F32) {
         const float f = __uint_as_float(scale[s][q] << 16);
-        float4* p = reinterpret_cast<float4*>(static_cast<float*>(dst) + off + 64 * q);
+        float4* p = reinterpret_cast<float4*>(static_cast<float*>(dst) + off + 64 * q - 4 * odd);
         const float2 x0 = __bfloat1622float2(n[0]), x1 = __bfloat1622float2(n[1]);
         const float2 x2 = __bfloat1622float2(n[2]), x3 = __bfloat1622float2(n[3]);
         __stcs(p, make_float4(f * x0.x, f * x0.y, f * x1.x, f * x1.y));
-        __stcs(p + 1, make_float4(f * x2.x, f * x2.y, f * x3.x, f * x3.y));
+        __stcs(p + 2, make_float4(f * x2.x, f * x2.y, f * x3.x, f * x3.y));
       } else {
         const uint32_t both = scale[s][q] | scale[s][q] << 16;
         const __nv_bfloat162 f = *reinterpret_cast<const __nv_bfloat162*>(&both);

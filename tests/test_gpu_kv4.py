@@ -171,6 +171,27 @@ def test_special_groups():
         np.testing.assert_array_equal(vb.double().cpu().numpy(), rv)
 
 
+def test_every_quotient_of_significands():
+    """All 128 significands of a group's largest element, of either sign, against every bf16
+    value from 2^-6 of it upwards: codes equal to exact rounding of the quotient, ties among
+    them."""
+    sig = np.arange(128, 256) / 128.0
+    small = np.concatenate([s * sig * 2.0 ** e for e in range(-6, 1) for s in (1, -1)])  # 1792 values
+    rows = []
+    for peak in sig:
+        x = small[np.abs(small) <= peak]
+        x = np.concatenate((x, np.zeros(-x.size % 30)))
+        g = np.zeros((x.size // 30, 32))
+        g[:, 0], g[:, 2:] = peak, x.reshape(-1, 30)
+        rows += [g, np.where(np.arange(32) == 0, -g, g)]
+    x = np.concatenate(rows)
+    x = np.concatenate((x, np.zeros((-len(x) % 8, 32)))).reshape(1, -1, 1, 256) * 2.0 ** 3
+    k, v = (torch.from_numpy(np.ascontiguousarray(x[..., i:i + 128])).cuda().bfloat16() for i in (0, 128))
+    c = Cache(1, x.shape[1], 1)
+    da.diffattn_kv4_write(k, v, c.t)
+    assert np.array_equal(c.entries(), plain.records(x[..., :128], x[..., 128:]))
+
+
 def test_strided_rows_and_cache():
     """K and V as slices of a fused projection, V1's K as [.., H, 2, 64], a cache with the
     heads outermost, and reads into slices whose surroundings stay as they are."""
