@@ -613,14 +613,14 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm)
             p[mt][j] = make_float2(ex2(y.x), ex2(y.y));
             l[j] = add2(l[j], p[mt][j]);
           }
-        // c by the sums so far at chunks 1, 2, 4, ..., and whenever it has come to be more than 4
-        // times lambda l_1 / l_2 in any lane's share of the keys (and so, at most, in all): past
-        // that its error would outgrow the one it saves. Lanes that disagree, as they do under
-        // peaked scores, make it small.
+        // c by the sums so far at chunks 1, 2, 4, 8, ..., and at every fourth where it has come to
+        // be more than 4 times lambda l_1 / l_2 in any lane's share of the keys (and so, at most,
+        // in all): past that its error would outgrow the one it saves. Lanes that disagree, as
+        // they do under peaked scores, make it small.
         const uint32_t nth = chunk - at + 1;
         const float mine1 = l[0].x + l[0].y, mine2 = l[1].x + l[1].y;
-        const bool large = fabsf(c) * mine2 > 4.f * fabsf(lam) * mine1;
-        if (__any_sync(0xffffffffu, large) || (nth & (nth - 1)) == 0) {
+        if (nth <= 2 || ((nth & 3u) == 0 && ((nth & (nth - 1)) == 0 ||
+                                             __any_sync(0xffffffffu, fabsf(c) * mine2 > 4.f * fabsf(lam) * mine1)))) {
           float s1 = mine1, s2 = mine2, least = mine2 > 0.f ? 4.f * __fdiv_rn(mine1, mine2) : INFINITY;
 #pragma unroll
           for (int s = 4; s <= 16; s <<= 1) {
