@@ -875,7 +875,7 @@ def diffattn_fwd_decode_kv4(q, cache, lam, kv_len=None, lambda_init=None, out=No
         if out is None:
             out = q.new_empty(shape)
         if workspace is None:
-            workspace = cache.new_empty(need)
+            workspace = cache.new_empty(need) if need else None
             ws_bytes = need
         else:
             if workspace.device != device or not workspace.is_contiguous():
@@ -884,7 +884,7 @@ def diffattn_fwd_decode_kv4(q, cache, lam, kv_len=None, lambda_init=None, out=No
         rc = lib.diffattn_fwd_decode_kv4(
             p, pk, q.data_ptr(), cache.data_ptr(), _addr(block_table), _addr(kv_len), lam.data_ptr(),
             _addr(lambda_init), int(v1 if apply_norm is None else bool(apply_norm)), norm_eps, out.data_ptr(),
-            workspace.data_ptr(), ws_bytes, _addr(dev_status), on.raw)
+            _addr(workspace), ws_bytes, _addr(dev_status), on.raw)
     _check("diffattn_fwd_decode_kv4", rc)
     return out
 

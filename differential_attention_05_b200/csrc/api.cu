@@ -733,8 +733,10 @@ int diffattn_fwd_decode_kv4(const diffattn_decode_params* p, const diffattn_page
   if (p->batch == 0) return DIFFATTN_OK;
   if (!q || !lambda || !out || (apply_norm && !lambda_init)) return DIFFATTN_ERR_INVALID_ARG;
   if (p->max_kv_len > 0 && (!cache || (pk && !block_table))) return DIFFATTN_ERR_INVALID_ARG;
-  if (!workspace || workspace_bytes < (size_t)a.states * 130 * sizeof(float)) return DIFFATTN_ERR_WORKSPACE;
-  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return DIFFATTN_ERR_MISALIGNED;
+  if (a.states) {
+    if (!workspace || workspace_bytes < (size_t)a.states * 130 * sizeof(float)) return DIFFATTN_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return DIFFATTN_ERR_MISALIGNED;
+  }
   if (!aligned16(q) || !aligned16(out)) return DIFFATTN_ERR_MISALIGNED;
   if (p->q_strides[0] % 8 || p->q_strides[1] % 8 || p->o_strides[0] % 8 || p->o_strides[1] % 8)
     return DIFFATTN_ERR_MISALIGNED;

@@ -166,6 +166,8 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 // copies of the full-size step alone took 473 us instead of 371.) A block finishes the entries
 // that lie within its range and leaves states for the others in the workspace: slot 0 for the
 // entry that began before its range, slot 1 for the one that goes on after it.
+// Short entries (by_entry) go whole to a group each, which needs no scan, no workspace and no
+// second kernel.
 __device__ __forceinline__ int kv4_len(const DecodeKv4Args& a, int b) {
   // device-side lengths are clamped into [0, L] so a bad value cannot read past the cache
   return a.kv_len ? min(max(__ldg(a.kv_len + b), 0), a.cache.L) : a.cache.L;
@@ -228,54 +230,73 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm)
   fence_barrier_init();
   cudaTriggerProgrammaticLaunchCompletion();
 
-  // this block's range and where it begins: chunks of the entries before each (`scan`, of THREADS
-  // entries at a time)
-  uint32_t T = 0, n = 0, scan = 0;
-  auto scan_entries = [&](int b0, uint32_t before) {  // returns the chunks up to their end
-    n = b0 + tid < a.B ? (kv4_len(a, b0 + tid) + CK - 1) / CK : 0;
-    scan = n;
+  int b = (int)group;
+  uint32_t range_begin = 0, range_end, entry_begin = 0;
+  if (a.by_entry) {
+    range_end = (kv4_len(a, b) + CK - 1) / CK;
+    __syncthreads();
+    if (range_end == 0) {  // no key: zeros
+      const int units = a.v1 ? 1 : min(ROWS, a.group - row0) / 2;
+      for (int i = tid; i < HB * units * W; i += THREADS) {
+        const int head = g0 + i / (units * W), unit = i / W % units;
+        const int64_t off = b * a.os[0] + (int64_t)(a.v1 ? head : (head * a.group + row0) / 2 + unit) * a.os[1] + i % W;
+        if (in_bounds(off, 1, a.ext_out, a.cache.dev_status, a.cache.dbg_status))
+          static_cast<__nv_bfloat16*>(a.out)[off] = __float2bfloat16_rn(0.f);
+      }
+      return;
+    }
+  } else {
+    // this block's range and where it begins: chunks of the entries before each (`scan`, of
+    // THREADS entries at a time)
+    uint32_t T = 0, n = 0, scan = 0;
+    auto scan_entries = [&](int b0, uint32_t before) {  // returns the chunks up to their end
+      n = b0 + tid < a.B ? (kv4_len(a, b0 + tid) + CK - 1) / CK : 0;
+      scan = n;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t up = __shfl_up_sync(0xffffffffu, scan, o);
-      if (lane >= o) scan += up;
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t up = __shfl_up_sync(0xffffffffu, scan, o);
+        if (lane >= o) scan += up;
+      }
+      if (lane == 31) sums[warp] = scan;
+      __syncthreads();
+      scan += before;
+      for (int w = 0; w < WARPS; ++w) {
+        if (w < warp) scan += sums[w];
+        before += sums[w];
+      }
+      __syncthreads();
+      return before;
+    };
+    if (!a.kv_len) {
+      n = (a.cache.L + CK - 1) / CK;
+      T = (uint32_t)a.B * n;
+    } else {
+      for (int b0 = 0; b0 < a.B; b0 += THREADS) T = scan_entries(b0, T);
     }
-    if (lane == 31) sums[warp] = scan;
-    __syncthreads();
-    scan += before;
-    for (int w = 0; w < WARPS; ++w) {
-      if (w < warp) scan += sums[w];
-      before += sums[w];
-    }
-    __syncthreads();
-    return before;
-  };
-  if (!a.kv_len) {
-    n = (a.cache.L + CK - 1) / CK;
-    T = (uint32_t)a.B * n;
-  } else {
-    for (int b0 = 0; b0 < a.B; b0 += THREADS) T = scan_entries(b0, T);
-  }
-  const Kv4Cuts cuts(T, a.groups);
-  const uint32_t range_begin = cuts.begin(group), range_end = cuts.begin(group + 1);
-  if (group >= min((uint32_t)a.groups, T)) return;
-  if (!a.kv_len) {
-    if (tid == 0) {
-      first[0] = range_begin / n;
-      first[1] = range_begin / n * n;
-    }
-  } else {
-    uint32_t before = 0;
-    for (int b0 = 0; b0 < a.B && before <= range_begin; b0 += THREADS) {
-      before = a.B <= THREADS ? T : scan_entries(b0, before);
-      if (scan - n <= range_begin && range_begin < scan) {
-        first[0] = b0 + tid;
-        first[1] = scan - n;
+    const Kv4Cuts cuts(T, a.groups);
+    range_begin = cuts.begin(group);
+    range_end = cuts.begin(group + 1);
+    if (group >= min((uint32_t)a.groups, T)) return;
+    if (!a.kv_len) {
+      if (tid == 0) {
+        first[0] = range_begin / n;
+        first[1] = range_begin / n * n;
+      }
+    } else {
+      uint32_t before = 0;
+      for (int b0 = 0; b0 < a.B && before <= range_begin; b0 += THREADS) {
+        before = a.B <= THREADS ? T : scan_entries(b0, before);
+        if (scan - n <= range_begin && range_begin < scan) {
+          first[0] = b0 + tid;
+          first[1] = scan - n;
+        }
       }
     }
+    __syncthreads();
+    b = (int)first[0];
+    entry_begin = first[1];
   }
-  __syncthreads();
-  int b = (int)first[0];
-  uint32_t at = range_begin, entry_begin = first[1];  // chunk in work, first one of its entry
+  uint32_t at = range_begin;  // chunk in work
   int stage = 0;
   uint32_t parity = 0;  // of the ring's current round
   auto advance = [&] {
@@ -934,20 +955,26 @@ static int kv4_heads(int H, int64_t head_stride) {
 
 // Groups of blocks (Kv4Cuts): `num_splits` for each entry on average if that is given, else as
 // many as run at once, but not so many that the chunks of full-length entries do not give each
-// kMin. States are kept for two entries of every block.
+// kMin. States are kept for two entries of every block. Entries stay whole up to 4 chunks, or as
+// many as an eighth of the blocks that gives, to 20: a chunk takes a block 0.8 us, what sharing
+// costs grows with the entries (64 entries x 8 heads of 300 tokens: 13 us whole, 19 shared; 8
+// entries 13 and 9; 600 tokens, 64 entries: 22 and 23).
 void decode_kv4_plan(DecodeKv4Args* a, int num_splits) {
   constexpr int64_t kMin = 2;
   a->heads = kv4_heads(a->H, a->cache.stride[2]);
-  const int64_t ck = KEYS * (CW / a->heads);
+  const int64_t ck = KEYS * (CW / a->heads), per_entry = (a->cache.L + ck - 1) / ck;
   const int64_t HQ = a->H / a->heads * ((a->group + ROWS - 1) / ROWS);
-  a->chunks = (int64_t)a->B * ((a->cache.L + ck - 1) / ck);
+  a->chunks = (int64_t)a->B * per_entry;
   int64_t groups = num_splits ? (int64_t)num_splits * a->B : 148 * kBlocksPerSm / HQ;
   const int64_t most = num_splits ? a->chunks : (a->chunks + kMin - 1) / kMin;
   if (groups > most) groups = most;
   if (groups > (1 << 16)) groups = 1 << 16;
+  const int64_t eighth = a->B * HQ / 8, whole = eighth < 4 ? 4 : (eighth < 20 ? eighth : 20);
+  a->by_entry = !num_splits && per_entry <= whole;
+  if (a->by_entry) groups = a->B;
   a->groups = groups < 1 ? 1 : (int)groups;
   a->blocks = a->groups * HQ;
-  a->states = a->blocks * 2 * a->heads * ROWS;
+  a->states = a->by_entry ? 0 : a->blocks * 2 * a->heads * ROWS;
 }
 
 // HB = 1: {144 bytes, heads, rows, entries or pages}, boxes of one head's records; else
@@ -1005,7 +1032,7 @@ static cudaError_t launch_split(const DecodeKv4Args& a, cudaStream_t stream) {
 cudaError_t launch_decode_kv4(const DecodeKv4Args& a, cudaStream_t stream) {
   const cudaError_t e =
       a.heads == 4 ? launch_split<4>(a, stream) : (a.heads == 2 ? launch_split<2>(a, stream) : launch_split<1>(a, stream));
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || a.by_entry) return e;
   // launched while the last blocks still run; the kernel waits for them itself
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -172,6 +172,7 @@ struct DecodeKv4Args {
   int v1;
   int group;              // query rows of a KV head: V1 2 (its branches), V2 Hq / H
   int heads, groups;      // KV heads of a block, groups of blocks (decode_kv4_plan)
+  int by_entry;           // every group takes one whole entry
   int64_t chunks;         // of full-length entries
   int64_t blocks, states; // of the launch; rows of the workspace
   int64_t qs[2], os[2];

@@ -540,7 +540,8 @@ int diffattn_kv4_read(const diffattn_kv4_rows* p, const diffattn_paged_kv* pk, c
  *   kv_len      : int32 [B] or NULL (NULL = max_kv_len), clamped to [0, max_kv_len]; 0 gives a
  *                 zero output row
  *   lambda_init, apply_norm, norm_eps : V1 as for diffattn_fwd_decode_v1; V2: apply_norm = 0
- *   workspace   : >= diffattn_decode_kv4_workspace_size(p, pk) bytes, 256-byte aligned; calls
+ *   workspace   : >= diffattn_decode_kv4_workspace_size(p, pk) bytes, 256-byte aligned (NULL where
+ *                 that is 0, as for short caches); calls
  *                 sharing a workspace must not overlap in time. Its size does not grow with
  *                 the lengths (at most 15 MB with num_splits = 0, up to 444
  *                 head tiles)

@@ -145,19 +145,23 @@ def test_decode_pointers_norm_and_workspace(lib):
     # the workspace: two units' states of every block, 4 heads of 8 rows each here
     n = ctypes.c_size_t(1)
     size = lib.diffattn_decode_kv4_workspace_size
-    for splits, L, blocks in ((1, 1000, 2), (3, 1000, 6), (0, 1000, 32), (0, 64, 2), (9, 64, 4), (2, 0, 1)):
+    for splits, L, blocks in ((1, 1000, 2), (3, 1000, 6), (0, 1000, 32), (0, 128, 0), (0, 129, 5), (9, 64, 4), (2, 0, 1)):
         p = _params(num_splits=splits, max_kv_len=L, kv_strides=(1000 * 4 * REC, 4 * REC, REC))
         assert size(ctypes.byref(p), None, ctypes.byref(n)) == 0
         assert n.value == blocks * 2 * 4 * 8 * 130 * 4, (splits, L)
     p = _params(max_kv_len=1 << 20, kv_strides=(4 * REC << 20, 4 * REC, REC), n_q_heads=64)
     assert size(ctypes.byref(p), None, ctypes.byref(n)) == 0 and n.value < 20 << 20
     # the layout takes part: heads that do not lie side by side go one to a block
-    assert size(ctypes.byref(_params()), ctypes.byref(_pool()), ctypes.byref(n)) == 0
-    assert n.value == 2 * 2 * 4 * 8 * 130 * 4
-    apart = _pool(page_strides=(16 * 4 * 160, 4 * 160, 160))
-    assert size(ctypes.byref(_params()), ctypes.byref(apart), ctypes.byref(n)) == 0
-    assert n.value == 4 * 2 * 1 * 8 * 130 * 4
-    p = _params()
+    p = _params(max_kv_len=2048, n_q_heads=16)
+    pk = _pool(max_pages_per_seq=128)
+    assert size(ctypes.byref(p), ctypes.byref(pk), ctypes.byref(n)) == 0
+    assert n.value == 64 * 2 * 4 * 8 * 130 * 4
+    apart = _pool(max_pages_per_seq=128, page_strides=(16 * 4 * 160, 4 * 160, 160))
+    assert size(ctypes.byref(p), ctypes.byref(apart), ctypes.byref(n)) == 0
+    assert n.value == 16 * 4 * 2 * 1 * 8 * 130 * 4
+    # short entries need none
+    assert _decode(lib, _params(batch=0), ws=None) == 0
+    p = _params(max_kv_len=2048, kv_strides=(2048 * 4 * REC, 4 * REC, REC))
     assert size(ctypes.byref(p), None, ctypes.byref(n)) == 0
     assert _decode(lib, p, ws=None) == -4
     assert _decode(lib, p, ws_bytes=n.value - 1) == -4
