@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm)
   }
   if (tid == 0) abort_flag = 0;
   fence_barrier_init();
-  cudaTriggerProgrammaticLaunchCompletion();
+  cudaTriggerProgrammaticLaunchCompletion();  // the join may be launched
 
   int b = (int)group;
   uint32_t range_begin = 0, range_end, entry_begin = 0;
@@ -1033,21 +1033,13 @@ cudaError_t launch_decode_kv4(const DecodeKv4Args& a, cudaStream_t stream) {
   const cudaError_t e =
       a.heads == 4 ? launch_split<4>(a, stream) : (a.heads == 2 ? launch_split<2>(a, stream) : launch_split<1>(a, stream));
   if (e != cudaSuccess || a.by_entry) return e;
-  // launched while the last blocks still run; the kernel waits for them itself
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg;
-  memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3(a.H * a.group / 2, a.B);
+  // launched while the last blocks still run; the kernel waits for them itself. (With the split
+  // kernel launched early too, behind the join of the call before, ragged batches took 45 us
+  // instead of 39: its blocks then hold the SMs that the join needs.)
   const bool many = a.groups > 64 * (int64_t)a.B, spread = many && !a.apply_norm;
-  cfg.blockDim = dim3(many ? 512 : 128);
-  if (spread) cfg.gridDim.z = W / 32;
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, spread ? decode_kv4_combine_kernel<16, 32>
-                                         : (many ? decode_kv4_combine_kernel<16, W> : decode_kv4_combine_kernel<4, W>), a);
+  return kv4_launch_early(spread ? decode_kv4_combine_kernel<16, 32>
+                                 : (many ? decode_kv4_combine_kernel<16, W> : decode_kv4_combine_kernel<4, W>),
+                          dim3(a.H * a.group / 2, a.B, spread ? W / 32 : 1), dim3(many ? 512 : 128), 0, stream, a);
 }
 
 }  // namespace diffattn

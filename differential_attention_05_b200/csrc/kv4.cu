@@ -126,6 +126,7 @@ template <bool F32>
 __global__ void __launch_bounds__(WARPS * 32) kv4_write_kernel(Kv4RowsArgs a) {
   constexpr int STEPS = F32 ? kStepsF32 : kSteps;
   const int b = blockIdx.y, lane = threadIdx.x & 31, sub = lane >> 4;
+  kv4_wait();
   const Kv4Entry e = kv4_entry(a, b);
   if (!e.ok) {
     if (blockIdx.x == 0 && threadIdx.x == 0) report_status(a.cache.dev_status, DIFFATTN_ERR_INVALID_ARG);
@@ -199,6 +200,7 @@ template <bool F32>
 __global__ void __launch_bounds__(WARPS * 32) kv4_read_kernel(Kv4RowsArgs a) {
   constexpr int STEPS = F32 ? kStepsF32 : kSteps;
   const int b = blockIdx.y, lane = threadIdx.x & 31, sub = lane >> 4;
+  kv4_wait();
   const Kv4Entry e = kv4_entry(a, b);
   if (!e.ok) {
     if (blockIdx.x == 0 && threadIdx.x == 0) report_status(a.cache.dev_status, DIFFATTN_ERR_INVALID_ARG);
@@ -273,8 +275,7 @@ static cudaError_t kv4_launch(Kv4RowsArgs a, void (*fn)(Kv4RowsArgs), int recs, 
   while ((2 << a.head_shift) <= recs && a.H % (2 << a.head_shift) == 0) ++a.head_shift;
   const int64_t rows = recs >> a.head_shift;
   const int64_t items = ((int64_t)a.N + rows - 1) / rows * (a.H >> a.head_shift);
-  fn<<<dim3((unsigned)((items + WARPS - 1) / WARPS), (unsigned)a.B), WARPS * 32, 0, stream>>>(a);
-  return cudaGetLastError();
+  return kv4_launch_early(fn, dim3((unsigned)((items + WARPS - 1) / WARPS), (unsigned)a.B), dim3(WARPS * 32), 0, stream, a);
 }
 
 cudaError_t launch_kv4_write(const Kv4RowsArgs& a, cudaStream_t stream) {
