@@ -351,6 +351,14 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm)
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
         }
+        // Not more than two chunks on their way: at the start all blocks would otherwise ask for a
+        // ring each, 34 MB, and the first chunk come in with the last (8 us into a ragged batch
+        // that the last block ended at 35; now 6 and 33)
+        if (issued >= 2) {
+          ok = mbar_wait(&full[(issued - 2) % STAGES], ((issued - 2) / STAGES) & 1u, &abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+        }
         if constexpr (LOAD == kTma) {
           if (lane == 0) {
             mbar_arrive_expect_tx(&full[stage], TL::STAGE_BYTES);
