@@ -670,46 +670,45 @@ def _kv4_plan(build, scalars, *tensors):
     return plan
 
 
-# the current stream's handle without a Stream object around it (6 us less a call), where this
-# torch has that
+# the current stream's handle without a Stream object around it (6 us less a call), and the
+# current device, where this torch has them
 try:
-    from torch._C import _cuda_getCurrentRawStream as _raw_stream
+    from torch._C import _cuda_getCurrentRawStream as _raw_stream, _cuda_getDevice as _get_device
 except ImportError:  # pragma: no cover
-    _raw_stream = None
+    _raw_stream = _get_device = None
 
 
 class _Kv4Scope:
-    """Makes the cache's device and the launch stream current where they are not, so that
-    allocations belong to that stream and a call on tensors of another device than the current
-    one lands there. `raw` is the launch stream's handle."""
+    """The launch stream's handle (`raw`), with the cache's device and that stream made current
+    until close() where they are not, so that allocations belong to the stream and a call on
+    tensors of another device than the current one lands there."""
 
-    __slots__ = ("device", "stream", "raw", "stack")
+    __slots__ = ("raw", "stack")
 
     def __init__(self, device, stream):
-        self.device, self.stream, self.stack = device, stream, None
-
-    def __enter__(self):
         import torch
-        stream, device = self.stream, self.device
         if stream is not None and stream.device != device:
             _kv4_fail("stream", f"the stream is on {stream.device}, the cache on {device}")
+        self.stack = None
         if stream is not None or torch.cuda.current_device() != device.index:
             import contextlib
             self.stack = contextlib.ExitStack()
             self.stack.enter_context(torch.cuda.device(device))
             if stream is not None:
                 self.stack.enter_context(torch.cuda.stream(stream))
-        if stream is not None:
-            self.raw = stream.cuda_stream
-        elif _raw_stream is not None:
-            self.raw = _raw_stream(device.index)
-        else:
-            self.raw = torch.cuda.current_stream(device).cuda_stream
-        return self
+        self.raw = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
 
-    def __exit__(self, *exc):
+    def close(self):
         if self.stack is not None:
-            self.stack.__exit__(*exc)
+            self.stack.close()
+
+
+def _kv4_scope(device, stream):
+    """(stream handle, scope to close or None): the common case without an object."""
+    if stream is None and _raw_stream is not None and _get_device() == device.index:
+        return _raw_stream(device.index), None
+    scope = _Kv4Scope(device, stream)
+    return scope.raw, scope
 
 
 def _int(x):
@@ -767,9 +766,13 @@ def diffattn_kv4_write(k, v, cache, pos=None, cu_seqlens=None, max_seqlen=None, 
     lib = load_library()
     p, pk, _ = _kv4_plan(_kv4_rows_plan, ("diffattn_kv4_write", _int(max_seqlen), _int(max_kv_len)), k, v, cache, pos,
                          cu_seqlens, block_table, dev_status)
-    with _Kv4Scope(cache.device, stream) as on:
+    raw, scope = _kv4_scope(cache.device, stream)
+    try:
         rc = lib.diffattn_kv4_write(p, pk, k.data_ptr(), v.data_ptr(), _addr(cu_seqlens), _addr(pos),
-                                    cache.data_ptr(), _addr(block_table), _addr(dev_status), on.raw)
+                                    cache.data_ptr(), _addr(block_table), _addr(dev_status), raw)
+    finally:
+        if scope is not None:
+            scope.close()
     _check("diffattn_kv4_write", rc)
     return cache
 
@@ -787,14 +790,16 @@ def diffattn_kv4_read(cache, n_tokens=None, pos=None, cu_seqlens=None, max_seqle
         _kv4_fail("diffattn_kv4_read", "give both k and v or neither")
     if not cache.is_cuda:
         _kv4_fail("diffattn_kv4_read", "cache is not a CUDA tensor")
-    with _Kv4Scope(cache.device, stream) as on:
+    device = cache.device
+    raw, scope = _kv4_scope(device, stream)
+    try:
         if k is None:
             if n_tokens is None or cache.dim() != 4:
                 _kv4_fail("diffattn_kv4_read", "needs n_tokens or k and v, and a cache [., ., H, 144]")
             rows = (int(n_tokens),)
             if cu_seqlens is None:
                 rows = (cache.shape[0] if block_table is None else block_table.shape[0], rows[0])
-            k = torch.empty((*rows, cache.shape[2], 128), dtype=dtype or torch.bfloat16, device=cache.device)
+            k = cache.new_empty((*rows, cache.shape[2], 128), dtype=dtype or torch.bfloat16)
             v = torch.empty_like(k)
         elif (n_tokens is not None and int(n_tokens) != k.shape[0 if cu_seqlens is not None else 1]) or (
                 dtype is not None and dtype != k.dtype):
@@ -802,7 +807,10 @@ def diffattn_kv4_read(cache, n_tokens=None, pos=None, cu_seqlens=None, max_seqle
         p, pk, _ = _kv4_plan(_kv4_rows_plan, ("diffattn_kv4_read", _int(max_seqlen), _int(max_kv_len)), k, v, cache, pos,
                              cu_seqlens, block_table, dev_status)
         rc = lib.diffattn_kv4_read(p, pk, cache.data_ptr(), _addr(block_table), _addr(cu_seqlens), _addr(pos),
-                                   k.data_ptr(), v.data_ptr(), _addr(dev_status), on.raw)
+                                   k.data_ptr(), v.data_ptr(), _addr(dev_status), raw)
+    finally:
+        if scope is not None:
+            scope.close()
     _check("diffattn_kv4_read", rc)
     return k, v
 
@@ -871,7 +879,8 @@ def diffattn_fwd_decode_kv4(q, cache, lam, kv_len=None, lambda_init=None, out=No
     p, pk, need, shape, v1, _ = _kv4_plan(_kv4_decode_plan, (int(num_splits), _int(max_kv_len)), q, cache, lam, kv_len,
                                           lambda_init, out, block_table, dev_status)
     device = cache.device
-    with _Kv4Scope(device, stream) as on:
+    raw, scope = _kv4_scope(device, stream)
+    try:
         if out is None:
             out = q.new_empty(shape)
         if workspace is None:
@@ -884,7 +893,10 @@ def diffattn_fwd_decode_kv4(q, cache, lam, kv_len=None, lambda_init=None, out=No
         rc = lib.diffattn_fwd_decode_kv4(
             p, pk, q.data_ptr(), cache.data_ptr(), _addr(block_table), _addr(kv_len), lam.data_ptr(),
             _addr(lambda_init), int(v1 if apply_norm is None else bool(apply_norm)), norm_eps, out.data_ptr(),
-            _addr(workspace), ws_bytes, _addr(dev_status), on.raw)
+            _addr(workspace), ws_bytes, _addr(dev_status), raw)
+    finally:
+        if scope is not None:
+            scope.close()
     _check("diffattn_fwd_decode_kv4", rc)
     return out
 
