@@ -541,16 +541,16 @@ int diffattn_kv4_read(const diffattn_kv4_rows* p, const diffattn_paged_kv* pk, c
  *                 zero output row
  *   lambda_init, apply_norm, norm_eps : V1 as for diffattn_fwd_decode_v1; V2: apply_norm = 0
  *   workspace   : >= diffattn_decode_kv4_workspace_size(p, pk) bytes, 256-byte aligned (NULL where
- *                 that is 0, as for short caches); calls
- *                 sharing a workspace must not overlap in time. Its size does not grow with
- *                 the lengths (at most 15 MB with num_splits = 0, up to 444
- *                 head tiles)
+ *                 that is 0, as for short caches); calls sharing a workspace must not overlap in
+ *                 time. Its size does not grow with the lengths (with num_splits = 0 at most 15
+ *                 MB, for up to 444 head tiles)
  * Arithmetic: q and the codes are exact MMA operands (q after a power-of-two scaling per row;
  * elements under 2^-31 of a row's largest lose bits, and rows with elements past 2^117
- * overflow), scales, sums and softmax statistics in fp32, probability times V scale rounded
- * once to fp16 (2^-11; products under 2^-22 of the row's largest probability times the
- * largest V scale lose bits, and with V past 2^100 small probabilities are dropped). No
- * atomics: results do not depend on scheduling.
+ * overflow), scales, sums and softmax statistics in fp32, probability times V scale (branch 1:
+ * p_1 - c p_2 with c near lambda l_1 / l_2, as in the prefill) rounded once to fp16 (2^-11;
+ * products under 2^-22 of the row's largest probability times the largest V scale lose bits,
+ * and with V past 2^100 small probabilities are dropped). No atomics: results do not depend on
+ * scheduling.
  * A block-table entry outside the pool is handled as by diffattn_fwd_decode_paged. Host-side
  * errors as for the other decodes.
  */

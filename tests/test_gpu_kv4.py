@@ -524,6 +524,48 @@ def test_decode_ragged_batches(H, page):
     _check_decode(2, *case, lens)
 
 
+@pytest.mark.parametrize("Hq,H", [(2, 1), (24, 2), (48, 3), (8, 4), (40, 4)])
+@pytest.mark.parametrize("page", [0, 1, 8, 32])
+def test_decode_short_caches(Hq, H, page):
+    """Entries short enough to stay whole in a block each: no workspace, and empty ones are
+    written as zeros; rows and heads around the output stay as they are."""
+    lens = [0, 1, 100, 33, 0, 64, 7]
+    c, rec, q, qx, lam = _decode_case(2, len(lens), Hq, H, 100, lens, page, seed=Hq + page)
+    assert da.diffattn_decode_kv4_workspace_size(*da._binding.decode_kv4_params(q, c.t, None, 0, c.table, 100)) == 0
+    wide = torch.full((len(lens), Hq // 2, 2, 128), 9.0, dtype=torch.bfloat16, device="cuda")
+    out = _check_decode(2, c, rec, q, qx, lam, lens, out=wide[:, :, 1])
+    assert (wide[:, :, 0] == 9.0).all() and (out[0] == 0).all() and (out[4] == 0).all()
+
+
+def test_two_threads():
+    """Two host threads, each on its own stream with its own cache, many calls at once; every
+    result equals the same call made alone."""
+    import threading
+    cases = [_decode_case(2, 2, 16, 2, n, [n, n // 2], seed=n) for n in (2000, 90)]
+
+    def call(i):
+        c, rec, q, qx, lam = cases[i]
+        da.diffattn_kv4_write(kv[i][0], kv[i][1], c.t, pos=_i32([5, 9]))
+        return da.diffattn_fwd_decode_kv4(q, c.t, torch.from_numpy(lam).cuda(), kv_len=_i32([c.L, c.L // 2]))
+
+    kv = [tuple(_rows(_rng(30 + i + j), (2, 1, 2, 128), torch.bfloat16)[0] for j in range(2)) for i in range(2)]
+    alone = [call(i).clone() for i in range(2)]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            outs = [call(i) for _ in range(30)]
+        s.synchronize()
+        wrong.extend(not torch.equal(o, alone[i]) for o in outs)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert len(wrong) == 60 and not any(wrong)
+
+
 @pytest.mark.parametrize("variant", [1, 2])
 def test_decode_large(variant):
     """The full-size step's cache length and heads at a smaller batch, against 64-bit products
