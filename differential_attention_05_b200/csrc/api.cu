@@ -626,7 +626,7 @@ static int kv4_rows_run(bool write, const diffattn_kv4_rows* p, const diffattn_p
                         const int32_t* block_table, int* dev_status, void* stream) {
   if (!p) return DIFFATTN_ERR_INVALID_ARG;
   if (p->dtype != DIFFATTN_F32 && p->dtype != DIFFATTN_BF16) return DIFFATTN_ERR_INVALID_ARG;
-  const int per = cu_seqlens ? p->max_seqlen : p->n_tokens;
+  const int per = cu_seqlens && p->max_seqlen < p->n_tokens ? p->max_seqlen : p->n_tokens;  // rows of an entry at most
   if (p->batch < 0 || p->n_tokens < 0 || per < 0 || p->n_kv_heads < 1 || p->max_kv_len < 0)
     return DIFFATTN_ERR_INVALID_ARG;
   if (p->batch > 65535 || p->n_kv_heads > 65535 || p->max_kv_len > (1 << 30)) return DIFFATTN_ERR_UNSUPPORTED;
