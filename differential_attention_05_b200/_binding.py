@@ -756,6 +756,21 @@ def _kv4_rows_plan(scalars, k, v, cache, pos, cu_seqlens, block_table, dev_statu
     return ctypes.pointer(p), None if pk is None else ctypes.cast(ctypes.pointer(pk), ctypes.c_void_p), pk
 
 
+def _kv4_read_plan(scalars, cache, pos, cu_seqlens, block_table, dev_status):
+    """The same of a read into new rows, and the shape, strides and type of these."""
+    import torch
+    fn = "diffattn_kv4_read"
+    n_tokens, dtype, max_seqlen, max_kv_len = scalars
+    if n_tokens is None or cache.dim() != 4:
+        _kv4_fail(fn, "needs n_tokens or k and v, and a cache [., ., H, 144]")
+    rows = (n_tokens,)
+    if cu_seqlens is None:
+        rows = (cache.shape[0] if block_table is None else block_table.shape[0], n_tokens)
+    k = cache.new_empty((*rows, cache.shape[2], 128), dtype=dtype or torch.bfloat16)
+    plan = _kv4_rows_plan((fn, max_seqlen, max_kv_len), k, k, cache, pos, cu_seqlens, block_table, dev_status)
+    return *plan, k.shape, k.stride(), k.dtype
+
+
 def diffattn_kv4_write(k, v, cache, pos=None, cu_seqlens=None, max_seqlen=None, block_table=None,
                        max_kv_len=None, dev_status=None, stream=None):
     """Quantise rows of K and V into a 4-bit cache (see include/diffattn.h): row i of entry b
@@ -794,18 +809,17 @@ def diffattn_kv4_read(cache, n_tokens=None, pos=None, cu_seqlens=None, max_seqle
     raw, scope = _kv4_scope(device, stream)
     try:
         if k is None:
-            if n_tokens is None or cache.dim() != 4:
-                _kv4_fail("diffattn_kv4_read", "needs n_tokens or k and v, and a cache [., ., H, 144]")
-            rows = (int(n_tokens),)
-            if cu_seqlens is None:
-                rows = (cache.shape[0] if block_table is None else block_table.shape[0], rows[0])
-            k = cache.new_empty((*rows, cache.shape[2], 128), dtype=dtype or torch.bfloat16)
+            p, pk, _, shape, strides, dtype = _kv4_plan(_kv4_read_plan, (_int(n_tokens), dtype, _int(max_seqlen),
+                                                                         _int(max_kv_len)), cache, pos, cu_seqlens,
+                                                        block_table, dev_status)
+            k = torch.empty_strided(shape, strides, dtype=dtype, device=device)
             v = torch.empty_like(k)
-        elif (n_tokens is not None and int(n_tokens) != k.shape[0 if cu_seqlens is not None else 1]) or (
-                dtype is not None and dtype != k.dtype):
-            _kv4_fail("diffattn_kv4_read", "n_tokens or dtype is not that of the given k")
-        p, pk, _ = _kv4_plan(_kv4_rows_plan, ("diffattn_kv4_read", _int(max_seqlen), _int(max_kv_len)), k, v, cache, pos,
-                             cu_seqlens, block_table, dev_status)
+        else:
+            if (n_tokens is not None and int(n_tokens) != k.shape[0 if cu_seqlens is not None else 1]) or (
+                    dtype is not None and dtype != k.dtype):
+                _kv4_fail("diffattn_kv4_read", "n_tokens or dtype is not that of the given k")
+            p, pk, _ = _kv4_plan(_kv4_rows_plan, ("diffattn_kv4_read", _int(max_seqlen), _int(max_kv_len)), k, v,
+                                 cache, pos, cu_seqlens, block_table, dev_status)
         rc = lib.diffattn_kv4_read(p, pk, cache.data_ptr(), _addr(block_table), _addr(cu_seqlens), _addr(pos),
                                    k.data_ptr(), v.data_ptr(), _addr(dev_status), raw)
     finally:
