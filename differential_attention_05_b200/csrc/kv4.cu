@@ -11,7 +11,7 @@
 // The kernels write n without a division for each element: with r = 1 / scale to 2^-23,
 // x r is within 2^-22 of x / scale in relative terms, and adding and taking away 1.5 * 2^11
 // rounds it to a multiple of 2^-12; a tie comes out exactly, and anything else stays on its
-// side of one (x / scale is at most 8 in magnitude and at least 2^-10 from a tie it does not
+// side of one (x / scale is at most 8 in magnitude and at least 2^-9 from a tie it does not
 // meet, having two 8-bit significands). A second such constant then rounds to an integer.
 //
 // Both kernels move bytes, and at first their index arithmetic cost more than the work on the

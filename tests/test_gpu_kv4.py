@@ -138,6 +138,33 @@ def test_write_and_read_packed(page, dtype):
         assert (got[-4:] == 7.0).all()
 
 
+def test_packed_rows_under_the_largest_max_seqlen():
+    """A caller that knows no better bound than int32's may give that one: the rows of the tensors
+    bound the launch. New rows of a read have the cache's heads and the type asked for."""
+    lens, H = [3, 0, 9], 2
+    rng = _rng(32)
+    c = Cache(3, 12, H, 4, seed=4)
+    want = c.entries().copy()
+    k, kx = _rows(rng, (12, H, 128), torch.bfloat16)
+    v, vx = _rows(rng, (12, H, 128), torch.bfloat16)
+    cu = _cu(lens)
+    da.diffattn_kv4_write(k, v, c.t, cu_seqlens=cu, max_seqlen=2**31 - 1, **c.where)
+    row = 0
+    for b, n in enumerate(lens):
+        want[b, :n] = plain.records(kx[row:row + n], vx[row:row + n])
+        row += n
+    assert np.array_equal(c.entries(), want)
+    rk, rv = plain.values(plain.records(kx, vx))
+    for dtype in (None, torch.float32):
+        for _ in range(2):  # the second call finds the first one's plan
+            got = da.diffattn_kv4_read(c.t, n_tokens=12, cu_seqlens=cu, max_seqlen=2**31 - 1, dtype=dtype, **c.where)
+            for x, ref in zip(got, (rk, rv)):
+                assert x.dtype == (dtype or torch.bfloat16) and x.shape == (12, H, 128) and x.is_contiguous()
+                ref = plain.bf16_round(ref) if dtype is None else ref
+                assert np.array_equal(x.double().cpu().numpy(), ref)
+            assert got[0].data_ptr() != got[1].data_ptr()
+
+
 def test_special_groups():
     """Zeros of both signs, +-ties, a lone element, NaN, infinities, the type's extremes,
     subnormals, values around the zero threshold, and ties between codes."""
