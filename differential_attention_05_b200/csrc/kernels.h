@@ -156,7 +156,6 @@ struct Kv4RowsArgs {
   int N;                  // rows of an entry; packed: the most rows of one
   int total;              // packed: rows of the tensors
   int f32;                // rows are fp32 (else bf16)
-  int head_shift;         // set by the launch: log2 of the heads a warp takes of a row
   const int32_t* cu;      // packed: [B + 1] offsets, else nullptr
   const int32_t* pos;     // [B] position of each entry's first row, or nullptr for 0
   void* k;                // read from (write) or written to (read)

@@ -14,20 +14,23 @@
 // side of one (x / scale is at most 8 in magnitude and at least 2^-9 from a tie it does not
 // meet, having two 8-bit significands). A second such constant then rounds to an integer.
 //
-// Both kernels move bytes, and at first their index arithmetic cost more than the work on the
-// channels (164 instructions a record, 107 us for 65536 tokens x 8 heads, with a warp to a
-// record). Now a half-warp takes a record: lanes 0..7 its K row, 8..15 its V row, each lane
-// channels 8 c .. 8 c + 7 and 64 more of them further on, so the rows are runs of 128 bytes
-// and four lanes share a scale. A warp takes 2 STEPS records, neighbouring heads first and
-// then the next tokens, with the loads of all in flight together.
+// Both kernels move bytes, and what bounds the write of bf16 rows is still issue slots: 97
+// instructions a record (65536 tokens x 8 heads, 61 us where the bytes need 53; 107 us with a
+// warp to a record and 164 instructions, 76 us with 125). Reading them takes 54 us, fp32 rows of
+// 16384 tokens 25 us either way for 24 of bytes. A half-warp takes a record: lanes 0..7 its K
+// row, 8..15 its V row, each lane channels 8 c .. 8 c + 7 and 64 more of them further on, so the
+// rows are runs of 128 bytes and four lanes share a scale. A warp takes 2 STEPS records,
+// neighbouring heads first and then the next tokens, with the loads of all in flight together.
 #include "kv4.cuh"
 
 namespace diffattn {
 
 namespace {
-constexpr int WARPS = 8;
-constexpr int kSteps = 4;     // pairs of records of a warp (bf16 rows)
-constexpr int kStepsF32 = 2;  // and of fp32 rows, twice as wide
+constexpr int WARPS = 4;
+// Pairs of records of a warp. Writing bf16 rows takes 61 us with 4 and 65 with 2 (65536 tokens x 8
+// heads), reading them 55 and 54; fp32 rows fill a warp's loads with one (16384 tokens: 24.7 and
+// 24.8 us, with two 25.3 and 25.6).
+constexpr int kWriteSteps = 4, kReadSteps = 2, kStepsF32 = 1;
 }  // namespace
 
 // The rows of entry b: their count and the first one's row in packed tensors. Offsets that
@@ -49,34 +52,41 @@ __device__ __forceinline__ Kv4Entry kv4_entry(const Kv4RowsArgs& a, int b) {
   return e;
 }
 
-// Where this lane's channels are: of record r of the warp's, in the K or V tensor (elements)
-// and in the cache (bytes; -1: its position or page is outside).
+// Where this lane's channels are: in the K or V tensor (elements) and in the cache (bytes). Of
+// the warp's 2 STEPS records, half-warp `sub` takes 2 s + sub at step s; SHIFT is the log2 of the
+// heads among them, so steps of one row share its position, page and offsets. (With SHIFT at run
+// time they were computed for every record, and the write of 65536 x 8 bf16 rows took 76 us, not 64.)
+template <int SHIFT>
 struct Kv4Lane {
   const Kv4RowsArgs& a;
-  int b, n, i0, h0, c, v;
-  int64_t pos, base, s1, s2;
+  int b, i0, c, v, sub;
+  int64_t pos, base, cache_base, s1, s2;
   __device__ __forceinline__ Kv4Lane(const Kv4RowsArgs& args, const Kv4Entry& e, int entry, int lane, int recs)
-      : a(args), b(entry), n(e.n) {
+      : a(args), b(entry) {
     const uint32_t item = blockIdx.x * WARPS + (threadIdx.x >> 5);
-    const uint32_t head_items = (uint32_t)a.H >> a.head_shift;
+    const uint32_t head_items = (uint32_t)a.H >> SHIFT;
     const uint32_t row_item = item / head_items;
-    i0 = (int)(row_item * (uint32_t)(recs >> a.head_shift));
-    h0 = (int)(item - row_item * head_items) << a.head_shift;
+    i0 = (int)(row_item * (uint32_t)(recs >> SHIFT));
     c = lane & 7;
     v = (lane >> 3) & 1;
+    sub = lane >> 4;
+    const int h0 = ((int)(item - row_item * head_items) << SHIFT) + (SHIFT ? sub : 0);
     pos = a.pos ? __ldg(a.pos + b) : 0;
     s1 = v ? a.vs[1] : a.ks[1];
     s2 = v ? a.vs[2] : a.ks[2];
-    base = (a.cu ? e.row0 * s1 : b * (v ? a.vs[0] : a.ks[0])) + c * 8;
+    base = (a.cu ? e.row0 * s1 : b * (v ? a.vs[0] : a.ks[0])) + h0 * s2 + c * 8;
+    cache_base = h0 * a.cache.stride[2];
   }
-  __device__ __forceinline__ int row(int r) const { return i0 + (r >> a.head_shift); }
-  __device__ __forceinline__ int head(int r) const { return h0 + (r & ((1 << a.head_shift) - 1)); }
-  __device__ __forceinline__ int64_t channels(int r) const { return base + row(r) * s1 + head(r) * s2; }
-  __device__ __forceinline__ int64_t record(int r) const {
-    const int64_t t = pos + row(r);
+  __device__ __forceinline__ int row(int s) const { return i0 + (SHIFT ? 2 * s >> SHIFT : 2 * s + sub); }
+  static __device__ __forceinline__ bool new_row(int s) { return s == 0 || SHIFT == 0 || 2 * s % (1 << SHIFT) == 0; }
+  // heads past the first step's
+  static __device__ __forceinline__ int head(int s) { return 2 * s % (1 << SHIFT); }
+  // the record of row i and the first step's head, or -1
+  __device__ __forceinline__ int64_t record(int i) const {
+    const int64_t t = pos + i;
     if (t < 0 || t >= a.cache.L) return -1;
     const int64_t at = kv4_page_offset(a.cache, b, (int)t);
-    return at < 0 ? -1 : at + head(r) * a.cache.stride[2];
+    return at < 0 ? -1 : at + cache_base;
   }
 };
 
@@ -93,8 +103,8 @@ __device__ __forceinline__ uint32_t kv4_encode(const uint32_t (&w)[4], uint32_t&
   // The largest magnitude among the group's positive values (low half) and among its
   // negative ones (high half), on bf16 bits: as signed 16-bit integers the largest is the
   // largest positive value, as unsigned ones the largest negative one.
-  const uint32_t up = __vmaxs2(__vmaxs2(__vmaxs2(w[0], w[1]), __vmaxs2(w[2], w[3])), 0u);
-  const uint32_t down = __vmaxu2(__vmaxu2(__vmaxu2(w[0], w[1]), __vmaxu2(w[2], w[3])), 0x80008000u) ^ 0x80008000u;
+  const uint32_t up = __vimax_s16x2_relu(__vimax3_s16x2(w[0], w[1], w[2]), w[3]);
+  const uint32_t down = __vimax3_u16x2(__vimax3_u16x2(w[0], w[1], w[2]), w[3], 0x80008000u) ^ 0x80008000u;
   uint32_t most = __vmaxu2(__byte_perm(up, down, 0x5410), __byte_perm(up, down, 0x7632));
   most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, 1));
   most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, 2));
@@ -122,17 +132,17 @@ __device__ __forceinline__ uint32_t kv4_encode(const uint32_t (&w)[4], uint32_t&
   return held ? __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x5410) : 0x88888888u;
 }
 
-template <bool F32>
-__global__ void __launch_bounds__(WARPS * 32) kv4_write_kernel(Kv4RowsArgs a) {
-  constexpr int STEPS = F32 ? kStepsF32 : kSteps;
-  const int b = blockIdx.y, lane = threadIdx.x & 31, sub = lane >> 4;
+template <bool F32, int SHIFT>
+__global__ void __launch_bounds__(WARPS * 32, 12) kv4_write_kernel(Kv4RowsArgs a) {
+  constexpr int STEPS = F32 ? kStepsF32 : kWriteSteps;
+  const int b = blockIdx.y, lane = threadIdx.x & 31;
   kv4_wait();
   const Kv4Entry e = kv4_entry(a, b);
   if (!e.ok) {
     if (blockIdx.x == 0 && threadIdx.x == 0) report_status(a.cache.dev_status, DIFFATTN_ERR_INVALID_ARG);
     return;
   }
-  const Kv4Lane at(a, e, b, lane, 2 * STEPS);
+  const Kv4Lane<SHIFT> at(a, e, b, lane, 2 * STEPS);
   if (at.i0 >= e.n) return;
   const int64_t ext = at.v ? a.ext_v : a.ext_k;
   const void* src = at.v ? a.v : a.k;
@@ -140,15 +150,20 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_write_kernel(Kv4RowsArgs a) {
   uint32_t raw[F32 ? 1 : STEPS][2][4];  // 8 channels and the 8 at 64 further on
   float4 wide[F32 ? STEPS : 1][2][2];
   int64_t dst[STEPS];  // byte offset of the record, -1: not written
+  int64_t place = -1, from = 0;
 #pragma unroll
   for (int s = 0; s < STEPS; ++s) {
-    const int r = 2 * s + sub;
-    const bool mine = at.row(r) < e.n;
-    dst[s] = mine ? at.record(r) : -1;
-    const int64_t off = at.channels(r);
+    if (at.new_row(s)) {
+      const int i = at.row(s);
+      place = i < e.n ? at.record(i) : -1;
+      if (i < e.n && place < 0 && (lane & 15) == 0) report_status(a.cache.dev_status, DIFFATTN_ERR_INVALID_ARG);
+      from = at.base + min(i, e.n - 1) * at.s1;  // rows past the entry load its last one and are not written
+    }
+    dst[s] = place < 0 ? -1 : place + at.head(s) * a.cache.stride[2];
+    const int64_t off = from + at.head(s) * at.s2;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      const bool ok = mine && in_bounds(off + 64 * q, 8, ext, a.cache.dev_status, a.cache.dbg_status);
+      const bool ok = in_bounds(off + 64 * q, 8, ext, a.cache.dev_status, a.cache.dbg_status);
       if constexpr (F32) {
         const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(src) + off + 64 * q);
         wide[s][q][0] = ok ? __ldcs(p) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -159,7 +174,6 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_write_kernel(Kv4RowsArgs a) {
         raw[s][q][0] = x.x; raw[s][q][1] = x.y; raw[s][q][2] = x.z; raw[s][q][3] = x.w;
       }
     }
-    if (mine && dst[s] < 0 && (lane & 15) == 0) report_status(a.cache.dev_status, DIFFATTN_ERR_INVALID_ARG);
     if (dst[s] >= 0 && !in_bounds(dst[s], kKv4Record, a.cache.ext, a.cache.dev_status, a.cache.dbg_status)) dst[s] = -1;
   }
 #pragma unroll
@@ -196,30 +210,33 @@ __device__ __forceinline__ __nv_bfloat162 kv4_pair(uint32_t w) {
 
 // Reading back: each lane turns 4 code bytes and their group's scale into 8 channels, twice:
 // scale * (n - 8) has 12 significant bits, exact in fp32 and rounded once to bf16 (nearest).
-template <bool F32>
+template <bool F32, int SHIFT>
 __global__ void __launch_bounds__(WARPS * 32) kv4_read_kernel(Kv4RowsArgs a) {
-  constexpr int STEPS = F32 ? kStepsF32 : kSteps;
-  const int b = blockIdx.y, lane = threadIdx.x & 31, sub = lane >> 4;
+  constexpr int STEPS = F32 ? kStepsF32 : kReadSteps;
+  const int b = blockIdx.y, lane = threadIdx.x & 31;
   kv4_wait();
   const Kv4Entry e = kv4_entry(a, b);
   if (!e.ok) {
     if (blockIdx.x == 0 && threadIdx.x == 0) report_status(a.cache.dev_status, DIFFATTN_ERR_INVALID_ARG);
     return;
   }
-  const Kv4Lane at(a, e, b, lane, 2 * STEPS);
+  const Kv4Lane<SHIFT> at(a, e, b, lane, 2 * STEPS);
   if (at.i0 >= e.n) return;
   const int64_t ext = at.v ? a.ext_v : a.ext_k;
   void* dst = at.v ? a.v : a.k;
 
   uint32_t codes[STEPS][2], scale[STEPS][2];  // scale: bf16 bits
+  int64_t place = -1;
 #pragma unroll
   for (int s = 0; s < STEPS; ++s) {
-    const int r = 2 * s + sub;
-    const bool mine = at.row(r) < e.n;
-    const int64_t from = mine ? at.record(r) : -1;
-    // outside the entry or the pool: the row reads as zeros
-    if (mine && from < 0 && (lane & 15) == 0) report_status(a.cache.dev_status, DIFFATTN_ERR_INVALID_ARG);
-    const bool ok = from >= 0 && in_bounds(from, kKv4Record, a.cache.ext, a.cache.dev_status, a.cache.dbg_status);
+    if (at.new_row(s)) {
+      const int i = at.row(s);
+      place = i < e.n ? at.record(i) : -1;
+      // outside the entry or the pool: the row reads as zeros
+      if (i < e.n && place < 0 && (lane & 15) == 0) report_status(a.cache.dev_status, DIFFATTN_ERR_INVALID_ARG);
+    }
+    const int64_t from = place + at.head(s) * a.cache.stride[2];
+    const bool ok = place >= 0 && in_bounds(from, kKv4Record, a.cache.ext, a.cache.dev_status, a.cache.dbg_status);
     const uint8_t* rec = a.cache.base + (ok ? from : 0);
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
@@ -227,9 +244,10 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_read_kernel(Kv4RowsArgs a) {
       scale[s][q] = ok ? __ldcs(reinterpret_cast<const uint16_t*>(rec + kKv4Scales) + at.v * 4 + 2 * q + (at.c >> 2)) : 0u;
     }
   }
+  int64_t to = 0;
 #pragma unroll
   for (int s = 0; s < STEPS; ++s) {
-    const int r = 2 * s + sub, odd = at.c & 1;
+    const int odd = at.c & 1;
     if constexpr (F32) {
       // a pair of lanes swaps halves of its 16 channels, so that a store of 16 bytes per lane
       // fills whole 32-byte sectors: channels 4 odd .. and 8 + 4 odd .. of the pair's
@@ -239,8 +257,9 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_read_kernel(Kv4RowsArgs a) {
         codes[s][q] = odd ? __byte_perm(other, codes[s][q], 0x7632) : __byte_perm(codes[s][q], other, 0x5410);
       }
     }
-    if (at.row(r) >= e.n) continue;
-    const int64_t off = at.channels(r);
+    if (at.new_row(s)) to = at.base + at.row(s) * at.s1;
+    if (at.row(s) >= e.n) continue;
+    const int64_t off = to + at.head(s) * at.s2;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       if (!in_bounds(off + 64 * q, 8, ext, a.cache.dev_status, a.cache.dbg_status)) continue;
@@ -269,23 +288,31 @@ __global__ void __launch_bounds__(WARPS * 32) kv4_read_kernel(Kv4RowsArgs a) {
   }
 }
 
-// A warp's records: 2^head_shift neighbouring heads (as many of its 2 STEPS as divide H) by rows.
-static cudaError_t kv4_launch(Kv4RowsArgs a, void (*fn)(Kv4RowsArgs), int recs, cudaStream_t stream) {
-  a.head_shift = 0;
-  while ((2 << a.head_shift) <= recs && a.H % (2 << a.head_shift) == 0) ++a.head_shift;
-  const int64_t rows = recs >> a.head_shift;
-  const int64_t items = ((int64_t)a.N + rows - 1) / rows * (a.H >> a.head_shift);
-  return kv4_launch_early(fn, dim3((unsigned)((items + WARPS - 1) / WARPS), (unsigned)a.B), dim3(WARPS * 32), 0, stream, a);
+// A warp's records: 2^shift neighbouring heads (as many of its 2 STEPS as divide H) by rows.
+template <size_t SHIFTS>
+static cudaError_t kv4_launch(const Kv4RowsArgs& a, void (*const (&fns)[SHIFTS])(Kv4RowsArgs), int recs,
+                              cudaStream_t stream) {
+  int shift = 0;
+  while (shift + 1 < (int)SHIFTS && a.H % (2 << shift) == 0) ++shift;
+  const int64_t rows = recs >> shift;
+  const int64_t items = ((int64_t)a.N + rows - 1) / rows * (a.H >> shift);
+  return kv4_launch_early(fns[shift], dim3((unsigned)((items + WARPS - 1) / WARPS), (unsigned)a.B), dim3(WARPS * 32), 0,
+                          stream, a);
 }
 
+using Kv4Kernel = void (*)(Kv4RowsArgs);
+
 cudaError_t launch_kv4_write(const Kv4RowsArgs& a, cudaStream_t stream) {
-  return a.f32 ? kv4_launch(a, kv4_write_kernel<true>, 2 * kStepsF32, stream)
-               : kv4_launch(a, kv4_write_kernel<false>, 2 * kSteps, stream);
+  static const Kv4Kernel f32[] = {kv4_write_kernel<true, 0>, kv4_write_kernel<true, 1>};
+  static const Kv4Kernel bf16[] = {kv4_write_kernel<false, 0>, kv4_write_kernel<false, 1>, kv4_write_kernel<false, 2>,
+                                   kv4_write_kernel<false, 3>};
+  return a.f32 ? kv4_launch(a, f32, 2 * kStepsF32, stream) : kv4_launch(a, bf16, 2 * kWriteSteps, stream);
 }
 
 cudaError_t launch_kv4_read(const Kv4RowsArgs& a, cudaStream_t stream) {
-  return a.f32 ? kv4_launch(a, kv4_read_kernel<true>, 2 * kStepsF32, stream)
-               : kv4_launch(a, kv4_read_kernel<false>, 2 * kSteps, stream);
+  static const Kv4Kernel f32[] = {kv4_read_kernel<true, 0>, kv4_read_kernel<true, 1>};
+  static const Kv4Kernel bf16[] = {kv4_read_kernel<false, 0>, kv4_read_kernel<false, 1>, kv4_read_kernel<false, 2>};
+  return a.f32 ? kv4_launch(a, f32, 2 * kStepsF32, stream) : kv4_launch(a, bf16, 2 * kReadSteps, stream);
 }
 
 }  // namespace diffattn
