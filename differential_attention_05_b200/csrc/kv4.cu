@@ -16,7 +16,7 @@
 //
 // Both kernels move bytes, and what bounds the write of bf16 rows is still issue slots: 97
 // instructions a record (65536 tokens x 8 heads, 61 us where the bytes need 53; 107 us with a
-// warp to a record and 164 instructions, 76 us with 125). Reading them takes 54 us, fp32 rows of
+// warp to a record and 164 instructions, 76 us with 125). Reading them takes 55 us, fp32 rows of
 // 16384 tokens 25 us either way for 24 of bytes. A half-warp takes a record: lanes 0..7 its K
 // row, 8..15 its V row, each lane channels 8 c .. 8 c + 7 and 64 more of them further on, so the
 // rows are runs of 128 bytes and four lanes share a scale. A warp takes 2 STEPS records,
@@ -27,10 +27,10 @@ namespace diffattn {
 
 namespace {
 constexpr int WARPS = 4;
-// Pairs of records of a warp. Writing bf16 rows takes 61 us with 4 and 65 with 2 (65536 tokens x 8
-// heads), reading them 55 and 54; fp32 rows fill a warp's loads with one (16384 tokens: 24.7 and
-// 24.8 us, with two 25.3 and 25.6).
-constexpr int kWriteSteps = 4, kReadSteps = 2, kStepsF32 = 1;
+// Pairs of records of a warp. Fewer make more blocks, of which a ragged batch leaves many without
+// rows: 13 packed chunks of 1 to 1531 tokens x 8 heads took 21.7 us with fp32 rows (1 pair; 2: 15.2)
+// and 12.0 read as bf16 (2 pairs; 4: 9.8), against 0.5 and 0.8 us gained on 16384 and 65536 tokens.
+constexpr int kSteps = 4, kStepsF32 = 2;
 }  // namespace
 
 // The rows of entry b: their count and the first one's row in packed tensors. Offsets that
@@ -134,7 +134,7 @@ __device__ __forceinline__ uint32_t kv4_encode(const uint32_t (&w)[4], uint32_t&
 
 template <bool F32, int SHIFT>
 __global__ void __launch_bounds__(WARPS * 32, 12) kv4_write_kernel(Kv4RowsArgs a) {
-  constexpr int STEPS = F32 ? kStepsF32 : kWriteSteps;
+  constexpr int STEPS = F32 ? kStepsF32 : kSteps;
   const int b = blockIdx.y, lane = threadIdx.x & 31;
   kv4_wait();
   const Kv4Entry e = kv4_entry(a, b);
@@ -212,7 +212,7 @@ __device__ __forceinline__ __nv_bfloat162 kv4_pair(uint32_t w) {
 // scale * (n - 8) has 12 significant bits, exact in fp32 and rounded once to bf16 (nearest).
 template <bool F32, int SHIFT>
 __global__ void __launch_bounds__(WARPS * 32) kv4_read_kernel(Kv4RowsArgs a) {
-  constexpr int STEPS = F32 ? kStepsF32 : kReadSteps;
+  constexpr int STEPS = F32 ? kStepsF32 : kSteps;
   const int b = blockIdx.y, lane = threadIdx.x & 31;
   kv4_wait();
   const Kv4Entry e = kv4_entry(a, b);
@@ -303,16 +303,17 @@ static cudaError_t kv4_launch(const Kv4RowsArgs& a, void (*const (&fns)[SHIFTS])
 using Kv4Kernel = void (*)(Kv4RowsArgs);
 
 cudaError_t launch_kv4_write(const Kv4RowsArgs& a, cudaStream_t stream) {
-  static const Kv4Kernel f32[] = {kv4_write_kernel<true, 0>, kv4_write_kernel<true, 1>};
+  static const Kv4Kernel f32[] = {kv4_write_kernel<true, 0>, kv4_write_kernel<true, 1>, kv4_write_kernel<true, 2>};
   static const Kv4Kernel bf16[] = {kv4_write_kernel<false, 0>, kv4_write_kernel<false, 1>, kv4_write_kernel<false, 2>,
                                    kv4_write_kernel<false, 3>};
-  return a.f32 ? kv4_launch(a, f32, 2 * kStepsF32, stream) : kv4_launch(a, bf16, 2 * kWriteSteps, stream);
+  return a.f32 ? kv4_launch(a, f32, 2 * kStepsF32, stream) : kv4_launch(a, bf16, 2 * kSteps, stream);
 }
 
 cudaError_t launch_kv4_read(const Kv4RowsArgs& a, cudaStream_t stream) {
-  static const Kv4Kernel f32[] = {kv4_read_kernel<true, 0>, kv4_read_kernel<true, 1>};
-  static const Kv4Kernel bf16[] = {kv4_read_kernel<false, 0>, kv4_read_kernel<false, 1>, kv4_read_kernel<false, 2>};
-  return a.f32 ? kv4_launch(a, f32, 2 * kStepsF32, stream) : kv4_launch(a, bf16, 2 * kReadSteps, stream);
+  static const Kv4Kernel f32[] = {kv4_read_kernel<true, 0>, kv4_read_kernel<true, 1>, kv4_read_kernel<true, 2>};
+  static const Kv4Kernel bf16[] = {kv4_read_kernel<false, 0>, kv4_read_kernel<false, 1>, kv4_read_kernel<false, 2>,
+                                   kv4_read_kernel<false, 3>};
+  return a.f32 ? kv4_launch(a, f32, 2 * kStepsF32, stream) : kv4_launch(a, bf16, 2 * kSteps, stream);
 }
 
 }  // namespace diffattn

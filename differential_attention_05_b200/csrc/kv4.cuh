@@ -33,7 +33,7 @@ static_assert(kKv4Record == kKv4Scales + 16 && kKv4Record % 16 == 0, "record lay
 // before them in the stream still runs, wait for all of it (kv4_wait) before they touch memory,
 // and let the next one come early in turn. Every block waits, so order along the stream is kept
 // whole; what overlaps is the launch (a prompt of 2 x 4096 tokens x 16 heads written and read
-// back: 35 us instead of 39).
+// back: 35 us instead of 39 when it was measured).
 __device__ __forceinline__ void kv4_wait() {
   cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
