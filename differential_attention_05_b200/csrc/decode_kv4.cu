@@ -34,18 +34,24 @@
 //   * The branches' rounding errors do not cancel in O_1 / l_1 - lambda O_2 / l_2, while the
 //     values may: with lambda near 1 and flat scores (V1's norm then scales the rest up) the
 //     output was 0.0027 off in relative terms where its bf16 rounding alone makes 0.0016. So
-//     the operand of branch 1 is p_1 - c p_2, formed in fp32, with c near lambda l_1 / l_2 and
-//     at most 1: D = O_1 - c O_2 carries errors of its own size only, those of O_2 cancel, and
-//     O_1 = D + c O_2 is put together in fp32 when the warp is done. Both branches of a unit
-//     are neighbouring columns of one lane, so this costs two instructions a chunk and a look
-//     at c at every fourth (453 us for 447 on the full step).
+//     the operand of branch 1 is p_1 - c p_2, formed in fp32: D = O_1 - c O_2 carries errors of
+//     its own size only, those of O_2 cancel as far as c is near lambda l_1 / l_2, and
+//     O_1 = D + c O_2 is put together in fp32 when the warp is done. c is that ratio of the
+//     sums so far (0 to 1), but no larger than lets 0 <= c p_2 <= p_1 for every key that meets
+//     it. That is what makes it safe: a key's rounding errors then move the output by at most
+//     2^-11 (p_1 - c p_2) / l_1 + 2^-11 |c / l_1 - lambda / l_2| p_2 <= 2^-11 (p_1 / l_1 +
+//     |lambda| p_2 / l_2) times its |v|, as with c = 0. (Held by the sums alone, at every
+//     fourth chunk, it let a branch 2 that rises behind a sink of both put errors of c p_2 into
+//     D that are many times O_1's own: 0.01 to 0.14 of the output.) Both branches of a unit are
+//     neighbouring columns of one lane, so this costs a dozen
+//     instructions a chunk (467 us for 447 on the full step).
 //   * q is taken times a power of two per row so that its largest element is in [2^14, 2^15);
 //     fp16 then holds every element above 2^-31 of the largest exactly.
 //
 // What bounds it: power, then issue slots. V2, 64 entries x 32768 tokens x 8 heads (2.42 GB, 374
-// us at the copy rate): 453 us alone at 1965 MHz, 510 to 530 us call after call, when the GPU
-// holds its 1000 W at 1665 MHz. 32 keys of a head are about 530 warp instructions, 224 of them
-// unpacking; with the data in L2 the same loop takes no less. V1, 32 x 32768 x 16: 448 us.
+// us at the copy rate): 467 us alone, 510 to 550 us call after call, when the GPU holds its 1000
+// W at 1665 MHz. 32 keys of a head are about 540 warp instructions, 224 of them unpacking; with
+// the data in L2 the same loop takes no less. V1, 32 x 32768 x 16: 461 us.
 #include <cuda_fp16.h>
 
 #include <string.h>
@@ -508,7 +514,8 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm)
     const bool is_unit = row0 + 2 * tq < a.group;  // columns 2 tq, 2 tq + 1: the branches of unit u
     const int u = a.v1 ? g : (g * a.group + row0 + 2 * tq) >> 1;
     const float lam = is_unit ? __ldg(a.lambda + u) : 0.f;
-    float c = 0.f;  // column 2 tq accumulates p_1 - c p_2
+    float c = 0.f;  // column 2 tq accumulates p_1 - c p_2; c >= 0, and c p_2 <= p_1 for every key
+    float c_room = INFINITY;  // that holds for keys with log2 (p_2 / p_1) up to here
     // [group][tile]: channels 32 g + 4 gq + 2 tile + {0, 1}; elements 0, 2 column 2 tq, 1, 3 the next
     float o[4][2][4];
 #pragma unroll
@@ -525,6 +532,7 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm)
         for (int i = 0; i < 4; ++i) o[gr][ti][i] = 0.f;
 
     int left = kv_len - (int)(at - entry_begin) * CK - part * KEYS;  // keys from this warp's first on
+    uint32_t look = at;  // the chunk at which c next goes by the sums
     for (uint32_t chunk = at; chunk < stop; ++chunk, left -= CK) {
       if (ok) {
         ok = mbar_wait(&full[stage], parity, &abort_flag);
@@ -624,9 +632,10 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm)
           }
           // D <- alpha_1 (D + c O_2) - c' alpha_2 O_2, O_2 <- alpha_2 O_2, c' for the new maxima
           const bool both = alpha[0] > 0.f && alpha[1] > 0.f;
-          const float next = both ? fminf(fmaxf(__fmul_rn(c, __fdiv_rn(alpha[0], alpha[1])), -1.f), 1.f) : 0.f;
+          const float next = both ? fminf(__fmul_rn(c, __fdiv_rn(alpha[0], alpha[1])), 1.f) : 0.f;
           const float back = __fmul_rn(alpha[0], c) - __fmul_rn(next, alpha[1]);
           c = next;
+          c_room = -__log2f(c);
 #pragma unroll
           for (int gr = 0; gr < 4; ++gr)
 #pragma unroll
@@ -637,34 +646,45 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm)
                 o[gr][ti][i + 1] *= alpha[1];
               }
         }
-        // p of the keys (gq, gq + 8) of each 16, per column
+        // p of the keys (gq, gq + 8) of each 16, per column, and the most of log2 (p_2 / p_1). (A
+        // NaN, as of two scores of -inf past the end, counts for nothing in that.)
         float2 p[2][2];
+        float apart = -INFINITY;
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
+        for (int mt = 0; mt < 2; ++mt) {
+          float2 y[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float2 y = fma2(make_float2(x[mt][j], x[mt][2 + j]),
-                                  make_float2(factor[j], factor[j]), bias[j]);
-            p[mt][j] = make_float2(ex2(y.x), ex2(y.y));
+            y[j] = fma2(make_float2(x[mt][j], x[mt][2 + j]), make_float2(factor[j], factor[j]), bias[j]);
+            p[mt][j] = make_float2(ex2(y[j].x), ex2(y[j].y));
             l[j] = add2(l[j], p[mt][j]);
           }
-        // c by the sums so far at chunks 1, 2, 4, 8, ..., and at every fourth where it has come to
-        // be more than 4 times lambda l_1 / l_2 in any lane's share of the keys (and so, at most,
-        // in all): past that its error would outgrow the one it saves. Lanes that disagree, as
-        // they do under peaked scores, make it small.
-        const uint32_t nth = chunk - at + 1;
-        const float mine1 = l[0].x + l[0].y, mine2 = l[1].x + l[1].y;
-        if (nth <= 2 || ((nth & 3u) == 0 && ((nth & (nth - 1)) == 0 ||
-                                             __any_sync(0xffffffffu, fabsf(c) * mine2 > 4.f * fabsf(lam) * mine1)))) {
-          float s1 = mine1, s2 = mine2, least = mine2 > 0.f ? 4.f * __fdiv_rn(mine1, mine2) : INFINITY;
+          apart = fmaxf(apart, fmaxf(y[1].x - y[0].x, y[1].y - y[0].y));
+        }
+        // c is lambda l_1 / l_2 by the sums at chunks 1, 4, 16, ..., and made smaller before the
+        // operand is formed wherever a key's c p_2 would pass its p_1, with a quarter to spare so
+        // that the next such key is rare (scattered scores: some 20 times in 295 chunks; 68
+        // without that and with a look at the sums at 1, 2, 4, 8, ...)
+        const bool by_sums = chunk == look;
+        if (by_sums || __any_sync(0xffffffffu, apart > c_room)) {
 #pragma unroll
-          for (int s = 4; s <= 16; s <<= 1) {
-            s1 += __shfl_xor_sync(0xffffffffu, s1, s);
-            s2 += __shfl_xor_sync(0xffffffffu, s2, s);
-            least = fminf(least, __shfl_xor_sync(0xffffffffu, least, s));
+          for (int s = 4; s <= 16; s <<= 1) apart = fmaxf(apart, __shfl_xor_sync(0xffffffffu, apart, s));
+          float next = c;
+          if (by_sums) {
+            look = at + 4 * (look - at) + 3;
+            float s1 = l[0].x + l[0].y, s2 = l[1].x + l[1].y;
+#pragma unroll
+            for (int s = 4; s <= 16; s <<= 1) {
+              s1 += __shfl_xor_sync(0xffffffffu, s1, s);
+              s2 += __shfl_xor_sync(0xffffffffu, s2, s);
+            }
+            next = s2 > 0.f ? fminf(fmaxf(__fmul_rn(lam, __fdiv_rn(s1, s2)), 0.f), 1.f) : 0.f;
+            c_room = -__log2f(next);
           }
-          const float ratio = s2 > 0.f ? fminf(__fdiv_rn(s1, s2), least) : 0.f;
-          const float next = fminf(fmaxf(__fmul_rn(lam, ratio), -1.f), 1.f);
+          if (apart > c_room) {
+            c_room = 1.25f * apart;
+            next = ex2(-c_room);
+          }
           const float back = c - next;
           c = next;
 #pragma unroll
