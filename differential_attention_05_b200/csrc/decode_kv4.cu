@@ -27,10 +27,13 @@
 //   * Scales stay outside the MMAs: a group is two k-steps, its fp32 sums are scaled and
 //     added; for V the probability is multiplied by the scale in fp32 and rounded to fp16
 //     once (2^-11 relative; bf16's 2^-8 would be amplified by the subtraction and V1's norm).
-//     fp16's range is kept by the running maximum: M bounds x + E, E the exponent of the
-//     largest V scale so far, so products lie under 2^(kTop + kSlack), and M is raised only
-//     when the bound would be passed. Products under 2^-22 of the largest probability times
-//     the largest scale become subnormal and lose bits.
+//     fp16's range is kept by the running maximum M of the scores and the exponent E of the
+//     largest V scale so far: p = 2^(x - M), and the operand is p 2^(kTop - E) times the scale,
+//     under 2^(kTop + kSlack). M is raised only when a score passes it by kSlack. Products under
+//     2^-22 of the largest probability times the largest scale become subnormal and lose bits.
+//     M and the sums of p follow the scores alone. (With 2^(kTop - E) as a part of p, which saves
+//     four instructions a chunk, a V scale 2^36 times those before it made all their
+//     probabilities flush to 0, in the sums too: 32 keys of V = 0 counted for nothing.)
 //   * The branches' rounding errors do not cancel in O_1 / l_1 - lambda O_2 / l_2, while the
 //     values may: with lambda near 1 and flat scores (V1's norm then scales the rest up) the
 //     output was 0.0027 off in relative terms where its bf16 rounding alone makes 0.0016. So
@@ -64,8 +67,10 @@ namespace diffattn {
 namespace {
 constexpr int W = kKv4Width;
 constexpr int KEYS = 32;      // keys that a warp takes of a chunk
-constexpr float kTop = 8.f;   // p * scale <= 2^kTop when the maximum is raised ...
-constexpr float kSlack = 6.f; // ... and <= 2^(kTop + kSlack) before: |(p_1 - c p_2) scale| <= 2^15
+constexpr int kTop = 8;       // p * scale <= 2^kTop in units of the largest V scale when the maximum is raised ...
+constexpr float kSlack = 6.f; // ... and <= 2^(kTop + kSlack) before, inside fp16's range
+constexpr int kLeastE = -102; // the exponent E of the V scales: scales that are held are 2^-103 and more
+constexpr float kJoin = 1.f / (1 << 30) / 64.f;  // see the join's weights
 
 // A block has CW warps that compute and one that issues the copies; three blocks to an SM.
 constexpr int CW = 4;
@@ -138,6 +143,10 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
+}
+// 2^(kTop - E) from a pair of bounds (E + 126) << 7 | 0x7f on the V scales' bf16 bits
+__device__ __forceinline__ float kv4_unit(uint32_t scale_bound) {
+  return __uint_as_float((uint32_t)(127 + kTop + 126 - (int)(scale_bound >> 23)) << 23);
 }
 // (w & mask) | magic in one LOP3: the constants come in registers (`Magic`), because with two
 // immediates the compiler makes two instructions of it, 64 more for a chunk's V codes
@@ -505,12 +514,12 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm)
 #pragma unroll
     for (int j = 0; j < 2; ++j) factor[j] = __shfl_sync(0xffffffffu, down, (2 * tq + j) * 4);
 
-    // columns 2 tq, 2 tq + 1: the running maximum plus kSlack; kTop - maximum - E, twice; sums of
+    // columns 2 tq, 2 tq + 1: the running maximum plus kSlack; minus the maximum, twice; sums of
     // p over the keys gq and gq + 8 of each 16
     float limit[2];
     float2 bias[2], l[2];
-    float bound_E = -90.f;
-    uint32_t scale_bound = 0;  // bf16 bits that no V scale so far passes, twice
+    uint32_t scale_bound = ((kLeastE + 126) << 7 | 0x7f) * 0x10001u;  // bf16 bits that no V scale so far passes, twice
+    float unit = kv4_unit(scale_bound);
     const bool is_unit = row0 + 2 * tq < a.group;  // columns 2 tq, 2 tq + 1: the branches of unit u
     const int u = a.v1 ? g : (g * a.group + row0 + 2 * tq) >> 1;
     const float lam = is_unit ? __ldg(a.lambda + u) : 0.f;
@@ -609,12 +618,12 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm)
           raise = raise || top[j] > limit[j];
         }
         if (__any_sync(0xffffffffu, raise)) {
-          // E: |scale| < 2^E for all V scales so far (not below -90, so that p does not overflow
-          // over rows of zeros)
+          // |scale| < 2^E for all V scales so far; `shrink` is 2^(E - new E)
           const uint32_t most = __reduce_max_sync(0xffffffffu, max(big & 0xffffu, big >> 16));
-          const float E = fmaxf((float)((int)(most >> 7) - 126), bound_E);
-          bound_E = E;
-          scale_bound = ((uint32_t)((int)E + 126) << 7 | 0x7fu) * 0x10001u;
+          const uint32_t was = scale_bound >> 23, now_E = max(most >> 7, was);  // E + 126
+          const float shrink = __uint_as_float((uint32_t)max(127 + (int)was - (int)now_E, 0) << 23);
+          scale_bound = (now_E << 7 | 0x7fu) * 0x10001u;
+          unit = kv4_unit(scale_bound);
           float alpha[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
@@ -623,7 +632,7 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm)
             for (int s = 4; s <= 16; s <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, s));
             // what p was weighted with is `bias`, to the last bit: alpha and M go by it
             const float now = fmaxf(limit[j] - kSlack, t);
-            const float to = now == -INFINITY ? kTop - E : kTop - E - now;
+            const float to = now == -INFINITY ? 0.f : -now;
             alpha[j] = limit[j] == -INFINITY ? 0.f : ex2(to - bias[j].x);
             limit[j] = now + kSlack;
             bias[j] = make_float2(to, to);
@@ -633,9 +642,11 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm)
           // D <- alpha_1 (D + c O_2) - c' alpha_2 O_2, O_2 <- alpha_2 O_2, c' for the new maxima
           const bool both = alpha[0] > 0.f && alpha[1] > 0.f;
           const float next = both ? fminf(__fmul_rn(c, __fdiv_rn(alpha[0], alpha[1])), 1.f) : 0.f;
-          const float back = __fmul_rn(alpha[0], c) - __fmul_rn(next, alpha[1]);
+          const float back = (__fmul_rn(alpha[0], c) - __fmul_rn(next, alpha[1])) * shrink;
           c = next;
           c_room = -__log2f(c);
+          alpha[0] *= shrink;
+          alpha[1] *= shrink;
 #pragma unroll
           for (int gr = 0; gr < 4; ++gr)
 #pragma unroll
@@ -694,9 +705,12 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm)
 #pragma unroll
               for (int i = 0; i < 4; i += 2) o[gr][ti][i] = fmaf(back, o[gr][ti][i + 1], o[gr][ti][i]);
         }
-        // the operand of column 2 tq, see c
+        // the operand of column 2 tq, see c; from here on in units of the V scales
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) p[mt][0] = fma2(p[mt][1], make_float2(-c, -c), p[mt][0]);
+        for (int mt = 0; mt < 2; ++mt) {
+          p[mt][0] = mul2(fma2(p[mt][1], make_float2(-c, -c), p[mt][0]), make_float2(unit, unit));
+          p[mt][1] = mul2(p[mt][1], make_float2(unit, unit));
+        }
 
         // O += (p scale)^T-fragments times V
 #pragma unroll
@@ -728,15 +742,8 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm)
       if (lane == 0) mbar_arrive(&empty[stage]);
       advance();
     }
-    // O_1 from D
-#pragma unroll
-    for (int gr = 0; gr < 4; ++gr)
-#pragma unroll
-      for (int ti = 0; ti < 2; ++ti)
-#pragma unroll
-        for (int i = 0; i < 4; i += 2) o[gr][ti][i] = fmaf(c, o[gr][ti][i + 1], o[gr][ti][i]);
-
-    // the sums of p over the warp, and M = -bias (-inf without a key) of the columns
+    // The state of the warp's keys: M = -bias (-inf without a key), the sum L of p, and O / L, which
+    // has the size of V whatever the sizes of the states that it will be joined with.
     float L[2], M[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -745,6 +752,19 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm)
       for (int s = 4; s <= 16; s <<= 1) L[j] += __shfl_xor_sync(0xffffffffu, L[j], s);
       M[j] = limit[j] == -INFINITY ? -INFINITY : -bias[j].x;
     }
+    const float i0 = L[0] == 0.f ? 0.f : __fdiv_rn(1.f, L[0]);
+    const float i1 = L[1] == 0.f ? 0.f : __fdiv_rn(1.f, L[1]);
+    const float scale = __fdiv_rn(1.f, unit);
+#pragma unroll
+    for (int gr = 0; gr < 4; ++gr)
+#pragma unroll
+      for (int ti = 0; ti < 2; ++ti)
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          // O_1 from D; rounded alone, so that equal branches with lambda = 1 give exactly 0
+          o[gr][ti][i] = __fmul_rn(__fmul_rn(fmaf(c, o[gr][ti][i + 1], o[gr][ti][i]), i0), scale);
+          o[gr][ti][i + 1] = __fmul_rn(__fmul_rn(o[gr][ti][i + 1], i1), scale);
+        }
     if constexpr (TL::PER_HEAD > 1) {
       // the head's other warps hand their states to its first
       constexpr int OTHERS = TL::PER_HEAD - 1;
@@ -773,10 +793,13 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm)
             // a state without keys, or with none above -inf, has M = -inf and nothing to add;
             // only a NaN among its sums is passed on
             const float top = fmaxf(M[j], other.x);
-            const float f0 = M[j] == -INFINITY ? 1.f : ex2(M[j] - top);
-            const float f1 = other.x == -INFINITY ? 1.f : ex2(other.x - top);
+            float f0 = __fmul_rn(L[j], M[j] == -INFINITY ? 1.f : ex2(M[j] - top));
+            float f1 = __fmul_rn(other.y, other.x == -INFINITY ? 1.f : ex2(other.x - top));
             M[j] = top;
-            L[j] = fmaf(L[j], f0, other.y * f1);
+            L[j] = f0 + f1;
+            const float inv = L[j] == 0.f ? 0.f : __fdiv_rn(1.f, L[j]);
+            f0 = __fmul_rn(f0, inv);
+            f1 = __fmul_rn(f1, inv);
 #pragma unroll
             for (int gr = 0; gr < 4; ++gr) {
               const float4 v = *reinterpret_cast<const float4*>(sm_o + row * W + gr * 32 + gq * 4);
@@ -792,17 +815,12 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm)
       const bool whole = entry_begin >= range_begin && entry_end <= range_end;
       if (whole) {
         // a unit's 128 channels lie in the 8 lanes of a column pair, 16 to each
-        const float i0 = L[0] == 0.f ? 0.f : __fdiv_rn(1.f, L[0]);
-        const float i1 = L[1] == 0.f ? 0.f : __fdiv_rn(1.f, L[1]);
         float y[4][4], ss = 0.f;
 #pragma unroll
         for (int gr = 0; gr < 4; ++gr)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            // rounded alone, so that equal branches with lambda = 1 give exactly 0
-            const float o1 = __fmul_rn(o[gr][i >> 1][2 * (i & 1)], i0);
-            const float o2 = __fmul_rn(o[gr][i >> 1][2 * (i & 1) + 1], i1);
-            y[gr][i] = fmaf(-lam, o2, o1);
+            y[gr][i] = fmaf(-lam, o[gr][i >> 1][2 * (i & 1) + 1], o[gr][i >> 1][2 * (i & 1)]);
             ss = fmaf(y[gr][i], y[gr][i], ss);
           }
         float f = 1.f;
@@ -940,12 +958,15 @@ __global__ void __launch_bounds__(32 * SLICES) decode_kv4_combine_kernel(DecodeK
     __syncthreads();
     if (tid < held) {
       const float4 v = state(s0 + tid);
-      // a state without keys has M = -inf and nothing to add; only a NaN is passed on
-      const float f0 = v.x == -INFINITY ? 1.f : ex2(v.x - M[0]), f1 = v.z == -INFINITY ? 1.f : ex2(v.z - M[1]);
+      // a state without keys has M = -inf and nothing to add; only a NaN is passed on. kJoin
+      // bounds the sum of all weights by 1: a key counts for at most 2^kSlack in a state's L,
+      // and an entry has 2^30 keys at most
+      const float f0 = __fmul_rn(__fmul_rn(v.y, kJoin), v.x == -INFINITY ? 1.f : ex2(v.x - M[0]));
+      const float f1 = __fmul_rn(__fmul_rn(v.w, kJoin), v.z == -INFINITY ? 1.f : ex2(v.z - M[1]));
       weight[0][tid] = f0;
       weight[1][tid] = f1;
-      L[0] = fmaf(v.y, f0, L[0]);
-      L[1] = fmaf(v.w, f1, L[1]);
+      L[0] += f0;
+      L[1] += f1;
     }
     __syncthreads();
 #pragma unroll 4

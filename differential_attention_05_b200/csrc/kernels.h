@@ -182,8 +182,8 @@ struct DecodeKv4Args {
   int apply_norm;
   float eps;
   void* out;
-  float* ws_o;            // [blocks, 2 slots, heads, 8 rows, 128]
-  float* ws_ml;           // [blocks, 2 slots, heads, 8 rows, 2]
+  float* ws_o;            // [blocks, 2 slots, heads, 8 rows, 128]: O / L
+  float* ws_ml;           // [blocks, 2 slots, heads, 8 rows, 2]: M, L
   int64_t ext_q, ext_out, ext_ws_o, ext_ws_ml;
 };
 

@@ -1,0 +1,74 @@
+"""The decode over a 4-bit cache whose V rows differ in size from key to key: the softmax's sums
+follow the scores alone, whatever the V scales. Against plain 64-bit attention over the cache's
+values, within kv4_plain.decode's bound."""
+import numpy as np
+import pytest
+import torch
+
+import kv4_plain as plain
+from test_gpu_kv4 import Cache, _check_decode, _rng, _rows
+
+pytestmark = pytest.mark.gpu
+
+
+def _sized(variant, H, size, seed, qscale=0.5):
+    """A cache of one entry with normal rows, V's times `size` [n], q and lambda."""
+    rng = _rng(seed)
+    n = size.size
+    kx = plain.bf16_round(rng.standard_normal((1, n, H, 128)))
+    vx = plain.bf16_round((rng.standard_normal((1, n, H, 128)) + 1.0) * size[None, :, None, None])
+    rec = plain.records(kx, vx)
+    q, qx = _rows(rng, (1, H, 2, 64) if variant == 1 else (1, 8 * H, 128), torch.bfloat16, qscale)
+    lam = rng.uniform(-0.3, 0.95, H if variant == 1 else 4 * H).astype(np.float32)
+    return Cache(1, n, H).set_entries(rec), rec, q, qx, lam
+
+
+@pytest.mark.parametrize("H", [1, 2, 4, 8])
+@pytest.mark.parametrize("power", [20, 36, 60, 90])
+def test_keys_of_zero_value_count(H, power):
+    """Half the keys have V = 0 and half V of 2^power, all with the same score, and the output is
+    half of it: the zeros first and last, and in turn by 32 (the keys of a warp's chunk) and by
+    blocks' shares."""
+    n = 1024
+    for run in (32, 64, 128, n // 2):
+        for first in (0, 1):
+            size = np.where((np.arange(n) // run + first) % 2, 2.0 ** power, 0.0)
+            case = _sized(2, H, size, run, qscale=0.0)
+            for splits in (1, 2, 4, 0):
+                out = _check_decode(2, *case, [n], num_splits=splits, what=f"{run} {first} {splits}")
+                assert torch.isfinite(out).all()
+
+
+@pytest.mark.parametrize("variant", [1, 2])
+@pytest.mark.parametrize("H", [1, 2, 4])
+def test_sizes_along_the_keys(variant, H):
+    """V rows that grow or shrink along the keys, over 2^40 to the whole range of the type."""
+    n = 640
+    for lo, hi in ((-20, 20), (-99, -50), (-99, 120), (60, 120)):
+        for size in (np.linspace(lo, hi, n), np.linspace(hi, lo, n), np.where(np.arange(n) < n // 2, lo, hi)):
+            # V1's norm squares the output in fp32, which holds sizes to 2^60 or so
+            norm = variant == 1 and abs(lo) < 40 and abs(hi) < 40
+            case = _sized(variant, H, np.exp2(size), 7)
+            for splits in (1, 3, 0):
+                _check_decode(variant, *case, [n], norm=norm, num_splits=splits, what=f"{lo} {hi} {splits}")
+
+
+@pytest.mark.parametrize("power", [-99, -88, 100, 120])
+def test_small_probabilities_at_the_ends_of_the_range(power):
+    """Scores over 20 powers of two with V at the smallest and the largest sizes: what lies far
+    below the largest probability still adds up."""
+    n = 2048
+    case = list(_sized(2, 4, np.full(n, 2.0 ** power), 8))
+    y = np.full(n, -14.0)
+    y[5] = 0.0
+    kx = np.repeat(np.repeat(y[None, :, None, None], 4, 2), 128, 3)
+    rec = case[1]
+    vx = plain.values(rec)[1]
+    vx[:, 5] = -vx[:, 5].mean(0)  # one key against many
+    case[1] = rec = plain.records(plain.bf16_round(kx), plain.bf16_round(vx))
+    case[0] = Cache(1, n, 4).set_entries(rec)
+    qx = np.full((1, 32, 128), np.sqrt(128) / 128 / np.log2(np.e))
+    case[3] = plain.bf16_round(qx)
+    case[2] = torch.from_numpy(case[3]).cuda().bfloat16()
+    for splits in (1, 4, 0):
+        _check_decode(2, *case, [n], num_splits=splits)
