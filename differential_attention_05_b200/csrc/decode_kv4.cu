@@ -618,8 +618,12 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm)
           raise = raise || top[j] > limit[j];
         }
         if (__any_sync(0xffffffffu, raise)) {
-          // |scale| < 2^E for all V scales so far; `shrink` is 2^(E - new E)
-          const uint32_t most = __reduce_max_sync(0xffffffffu, max(big & 0xffffu, big >> 16));
+          // |scale| < 2^E for all finite V scales so far; `shrink` is 2^(E - new E). A NaN's (or
+          // an infinity's) own group is lost whatever E is, and the others' products go by theirs.
+          const uint2 all = *reinterpret_cast<const uint2*>(st + lane * PITCH + kKv4Scales + 8);
+          const uint32_t a0 = all.x & 0x7fff7fffu, a1 = all.y & 0x7fff7fffu;
+          const uint32_t held = __vmaxu2(a0 & __vcmpltu2(a0, 0x7f807f80u), a1 & __vcmpltu2(a1, 0x7f807f80u));
+          const uint32_t most = __reduce_max_sync(0xffffffffu, max(held & 0xffffu, held >> 16));
           const uint32_t was = scale_bound >> 23, now_E = max(most >> 7, was);  // E + 126
           const float shrink = __uint_as_float((uint32_t)max(127 + (int)was - (int)now_E, 0) << 23);
           scale_bound = (now_E << 7 | 0x7fu) * 0x10001u;

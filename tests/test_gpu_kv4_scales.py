@@ -5,6 +5,8 @@ import numpy as np
 import pytest
 import torch
 
+import differential_attention_05_b200 as da
+
 import kv4_plain as plain
 from test_gpu_kv4 import Cache, _check_decode, _rng, _rows
 
@@ -72,3 +74,35 @@ def test_small_probabilities_at_the_ends_of_the_range(power):
     case[2] = torch.from_numpy(case[3]).cuda().bfloat16()
     for splits in (1, 4, 0):
         _check_decode(2, *case, [n], num_splits=splits)
+
+
+@pytest.mark.parametrize("variant", [1, 2])
+@pytest.mark.parametrize("H", [1, 2, 4, 8])
+def test_a_nan_stays_in_its_group_of_channels(variant, H):
+    """Rows with a NaN or an infinity, as the write holds them: their groups of 32 channels come
+    out as NaN for every query of the head, all other channels as without them."""
+    n, B = 600, 3
+    rng = _rng(50 + H)
+    k, v = (plain.bf16_round(rng.standard_normal((B, n, H, 128))) for _ in range(2))
+    lost = np.zeros((B, H, 4), bool)
+    for b, t, h, c, x in ((0, 0, 0, 5, np.nan), (0, 470, 0, 40, np.inf), (1, 301, H - 1, 127, -np.inf),
+                          (1, 302, H - 1, 127, np.nan), (2, 599, H // 2, 70, np.nan), (2, 40, H // 2, 0, np.inf)):
+        v[b, t, h, c] = x
+        lost[b, h, c // 32] = True
+    rec = plain.records(k, v)
+    c = Cache(B, n, H)
+    t = [torch.from_numpy(x).cuda().bfloat16() for x in (k, v)]
+    da.diffattn_kv4_write(*t, c.t)
+    assert np.array_equal(c.entries(), rec)
+    q, qx = _rows(rng, (B, H, 2, 64) if variant == 1 else (B, 8 * H, 128), torch.bfloat16, 0.5)
+    units = H if variant == 1 else 4 * H
+    lam = rng.uniform(0.3, 0.95, units).astype(np.float32)
+    ref, bound = plain.decode(qx, plain.records(k, np.where(np.isfinite(v), v, 0.0)), lam.astype(np.float64), [n] * B, variant)
+    # the channels that are compared are the other groups', whose codes are the same in both
+    gone = np.repeat(np.repeat(lost, units // H, 1), 32, 2)
+    kv_len = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    for splits in (0, 1, 4):
+        out = da.diffattn_fwd_decode_kv4(q, c.t, torch.from_numpy(lam).cuda(), kv_len=kv_len, apply_norm=False,
+                                         num_splits=splits).double().cpu().numpy()
+        assert np.isnan(out[gone]).all()
+        assert (np.abs(out - ref)[~gone] <= bound[~gone]).all(), splits
