@@ -865,12 +865,13 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm)
 }
 
 // The output of one unit (V1 head or V2 pair) from its branches' attention outputs, channel
-// `c` of the W threads with `mine`: the difference, and V1's norm and scale. All threads of the
-// block take part; `red` holds 4 floats.
-__device__ __forceinline__ void store_unit(const DecodeKv4Args& a, int b, int u, int c, bool mine, float o1,
+// `c` of the W threads with `mine`: the difference, and V1's norm and scale; zero for an entry
+// without `keys`, whatever lambda and eps are. All threads of the block take part; `red` holds 4
+// floats.
+__device__ __forceinline__ void store_unit(const DecodeKv4Args& a, int b, int u, int c, bool mine, bool keys, float o1,
                                            float o2, float* red) {
-  float y = o1 - __ldg(a.lambda + u) * o2;
-  if (a.apply_norm) {
+  float y = keys ? o1 - __ldg(a.lambda + u) * o2 : 0.f;
+  if (a.apply_norm && keys) {
     const float ss = warp_sum(y * y);
     if (mine && (c & 31) == 0) red[c >> 5] = ss;
     __syncthreads();
@@ -1001,7 +1002,7 @@ __global__ void __launch_bounds__(32 * SLICES) decode_kv4_combine_kernel(DecodeK
     res[e] = l == 0.f ? 0.f : o / l;
   }
   __syncthreads();
-  store_unit(a, b, u, c0 + c, tid < CH, res[0], res[1], red[0]);
+  store_unit(a, b, u, c0 + c, tid < CH, n != 0, res[0], res[1], red[0]);
 }
 
 // Heads of a block: neighbours read together (one run of 144 HB bytes per token) when the

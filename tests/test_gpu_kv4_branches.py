@@ -10,6 +10,8 @@ import numpy as np
 import pytest
 import torch
 
+import differential_attention_05_b200 as da
+
 import kv4_plain as plain
 from test_gpu_kv4 import Cache, _check_decode, _rng
 
@@ -107,3 +109,26 @@ def test_branches_on_keys_of_their_own(variant):
             case = _scored(variant, y, 4, run)
             for splits in (1, 5):
                 _check_decode(variant, *case, [n], num_splits=splits, what=f"{run} {first} {splits}")
+
+
+@pytest.mark.parametrize("variant", [1, 2])
+@pytest.mark.parametrize("L", [40, 3000])
+def test_empty_entries_are_zero_whatever_lambda_and_eps(variant, L):
+    """No key gives a zero row: with norm_eps = 0, which the norm would divide by, and a lambda
+    that is no number; in caches short enough to stay whole and in ones that are shared."""
+    B, H = 3, 2
+    rng = _rng(60)
+    rec = plain.records(*(plain.bf16_round(rng.standard_normal((B, L, H, 128))) for _ in range(2)))
+    c = Cache(B, L, H).set_entries(rec)
+    units = H if variant == 1 else 4 * H
+    q = torch.randn((B, H, 2, 64) if variant == 1 else (B, 8 * H, 128), device="cuda").bfloat16()
+    lam = torch.full((units,), 0.5, device="cuda")
+    lam[1] = float("nan")
+    kv_len = torch.tensor([0, L, 0], dtype=torch.int32, device="cuda")
+    li = torch.full((1,), 0.2, device="cuda") if variant == 1 else None
+    for splits in (0, 1, 3):
+        for lens in (kv_len, torch.zeros_like(kv_len)):
+            out = da.diffattn_fwd_decode_kv4(q, c.t, lam, kv_len=lens, lambda_init=li, norm_eps=0.0, num_splits=splits)
+            empty = lens == 0
+            assert (out[empty] == 0).all(), splits
+            assert torch.isfinite(out[~empty][:, [0]]).all() and out[~empty][:, 1].isnan().all()
