@@ -29,8 +29,9 @@
 //     once (2^-11 relative; bf16's 2^-8 would be amplified by the subtraction and V1's norm).
 //     fp16's range is kept by the running maximum M of the scores and the exponent E of the
 //     largest V scale so far: p = 2^(x - M), and the operand is p 2^(kTop - E) times the scale,
-//     under 2^(kTop + kSlack). M is raised only when a score passes it by kSlack. Products under
-//     2^-22 of the largest probability times the largest scale become subnormal and lose bits.
+//     under 2^(kTop + kSlack). M is raised only when a score passes it by kSlack. The largest
+//     scale is 2^(E - 1) or more, so the largest probability times it makes an operand of 2^8 or
+//     more, and products under 2^-22 of that become subnormal and lose bits.
 //     M and the sums of p follow the scores alone. (With 2^(kTop - E) as a part of p, which saves
 //     four instructions a chunk, a V scale 2^36 times those before it made all their
 //     probabilities flush to 0, in the sums too: 32 keys of V = 0 counted for nothing.)
@@ -49,7 +50,8 @@
 //     neighbouring columns of one lane, so this costs a dozen
 //     instructions a chunk (467 us for 447 on the full step).
 //   * q is taken times a power of two per row so that its largest element is in [2^14, 2^15);
-//     fp16 then holds every element above 2^-31 of the largest exactly.
+//     fp16 then holds elements above 2^-31 of the largest exactly in even channels, and above
+//     2^-27 in odd ones, which are divided by 16.
 //
 // What bounds it: power, then issue slots. V2, 64 entries x 32768 tokens x 8 heads (2.42 GB, 374
 // us at the copy rate): 467 us alone, 510 to 550 us call after call, when the GPU holds its 1000
@@ -67,8 +69,8 @@ namespace diffattn {
 namespace {
 constexpr int W = kKv4Width;
 constexpr int KEYS = 32;      // keys that a warp takes of a chunk
-constexpr int kTop = 8;       // p * scale <= 2^kTop in units of the largest V scale when the maximum is raised ...
-constexpr float kSlack = 6.f; // ... and <= 2^(kTop + kSlack) before, inside fp16's range
+constexpr int kTop = 9;       // p * scale < 2^kTop in units of 2^E when the maximum is raised ...
+constexpr float kSlack = 6.f; // ... and < 2^(kTop + kSlack) before, inside fp16's range: p_1 - c p_2 <= p_1
 constexpr int kLeastE = -102; // the exponent E of the V scales: scales that are held are 2^-103 and more
 constexpr float kJoin = 1.f / (1 << 30) / 64.f;  // see the join's weights
 

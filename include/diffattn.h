@@ -545,7 +545,7 @@ int diffattn_kv4_read(const diffattn_kv4_rows* p, const diffattn_paged_kv* pk, c
  *                 time. Its size does not grow with the lengths (with num_splits = 0 at most 15
  *                 MB, for up to 444 head tiles)
  * Arithmetic: q and the codes are exact MMA operands (q after a power-of-two scaling per row;
- * elements under 2^-31 of a row's largest lose bits, and rows with elements past 2^117
+ * elements under 2^-27 of a row's largest lose bits, and rows with elements past 2^117
  * overflow), scales, sums and softmax statistics in fp32, probability times V scale (branch 1:
  * p_1 - c p_2 with c near lambda l_1 / l_2, as in the prefill, but no larger than keeps c p_2
  * <= p_1 for every key, so that no key's rounding counts for more than with c = 0) rounded once

@@ -106,3 +106,42 @@ def test_a_nan_stays_in_its_group_of_channels(variant, H):
                                          num_splits=splits).double().cpu().numpy()
         assert np.isnan(out[gone]).all()
         assert (np.abs(out - ref)[~gone] <= bound[~gone]).all(), splits
+
+
+def test_products_far_below_the_largest():
+    """One key has the largest probability and the largest V scale, just over a power of two, but
+    the value 0 outside channels 0, 32, 64 and 96; all others have products of 2^-29 to 2^-33 of
+    that, every key of an entry the same, so that their fp16 roundings add up: still no more than
+    2^-25 each where the largest product is 2^8."""
+    B, n, H = 48, 512, 4
+    y = np.linspace(-24.0, -28.0, B)
+    kx = np.repeat(np.repeat(np.repeat(y[:, None, None, None], n, 1), H, 2), 128, 3)
+    vx = np.full((B, n, H, 128), 2.0 ** -5)
+    kx[:, 7], vx[:, 7] = 0.0, 0.0
+    vx[:, 7, :, ::32] = 8.0625
+    vx[:, :7, :, 1::2] *= -1.0
+    rec = plain.records(plain.bf16_round(kx), plain.bf16_round(vx))
+    qx = plain.bf16_round(np.full((B, 2 * H, 128), np.sqrt(128) / 128 / np.log2(np.e)))
+    lam = np.zeros(H, np.float32)
+    q = torch.from_numpy(qx).cuda().bfloat16()
+    for splits in (1, 0):
+        _check_decode(2, Cache(B, n, H).set_entries(rec), rec, q, qx, lam, [n] * B, num_splits=splits)
+
+
+@pytest.mark.parametrize("channel,power", [(32, -31), (33, -27), (62, -30), (95, -26)])
+def test_small_elements_of_q_that_count(channel, power):
+    """A row of q whose largest element meets small keys, while one at the least size that is
+    held exactly in its channel decides the scores, over keys as much larger."""
+    n, H = 700, 2
+    rng = _rng(70)
+    for size in (1.0, 1.9921875):  # all bits of the significand
+        qx = np.zeros((1, 4 * H, 128))
+        qx[..., 0] = 1.0
+        qx[..., channel] = size * 2.0 ** power
+        kx = rng.standard_normal((1, n, H, 128)) * 2.0 ** -20
+        at = channel // 32 * 32
+        kx[..., at:at + 32] = rng.uniform(-30, 30, (1, n, H, 32)) * 2.0 ** -power
+        vx = rng.standard_normal((1, n, H, 128))
+        rec = plain.records(plain.bf16_round(kx), plain.bf16_round(vx))
+        q = torch.from_numpy(qx).cuda().bfloat16()
+        _check_decode(2, Cache(1, n, H).set_entries(rec), rec, q, qx, np.full(2 * H, 0.5, np.float32), [n])
