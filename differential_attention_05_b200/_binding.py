@@ -721,21 +721,28 @@ def _addr(t):
 
 def _kv4_rows_plan(scalars, k, v, cache, pos, cu_seqlens, block_table, dev_status):
     """(parameter struct, pool geometry or None) of a write or a read of rows k and v."""
-    import torch
     fn, max_seqlen, max_kv_len = scalars
-    packed = cu_seqlens is not None
-    lead = 1 if packed else 2
+    lead = 1 if cu_seqlens is not None else 2
     for name, t in (("k", k), ("v", v)):
         _kv4_tensor(fn, name, t, k.dtype, cache.device, dense=False)
         if t.dim() not in (lead + 2, lead + 3) or t.shape[lead + 1:].numel() != 128:
             _kv4_fail(fn, f"{name} has shape {tuple(t.shape)}: rows of 128 channels behind "
-                          + ("[rows, heads]" if packed else "[batch, rows, heads]"))
+                          + ("[rows, heads]" if lead == 1 else "[batch, rows, heads]"))
         if t.stride(-1) != 1 or (t.dim() == lead + 3 and t.stride(-2) != t.shape[-1]):
             _kv4_fail(fn, f"the 128 channels of {name} must be contiguous")
         if t.shape[:lead + 1] != k.shape[:lead + 1]:
             _kv4_fail(fn, f"k and v differ in rows or heads: {tuple(k.shape)}, {tuple(v.shape)}")
     if cache.dim() == 4 and k.shape[lead] != cache.shape[2]:
         _kv4_fail(fn, f"k has {k.shape[lead]} heads, the cache {cache.shape[2]}")
+    return _kv4_rows_params(fn, _dtype_code(k), k.shape[:lead + 1], k.stride()[:lead + 1], v.stride()[:lead + 1],
+                            max_seqlen, max_kv_len, cache, pos, cu_seqlens, block_table, dev_status)
+
+
+def _kv4_rows_params(fn, dtype, shape, k_strides, v_strides, max_seqlen, max_kv_len, cache, pos, cu_seqlens,
+                     block_table, dev_status):
+    """The same of rows [batch, rows, heads] or packed [rows, heads] by their shape, strides and type."""
+    import torch
+    packed = cu_seqlens is not None
     if packed:
         if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
             _kv4_fail(fn, "cu_seqlens must be [batch + 1]")
@@ -743,13 +750,13 @@ def _kv4_rows_plan(scalars, k, v, cache, pos, cu_seqlens, block_table, dev_statu
         if max_seqlen is None:
             _kv4_fail(fn, "cu_seqlens needs max_seqlen, the most rows of an entry")
     p = Kv4Rows()
-    p.dtype = _dtype_code(k)
-    p.batch = int(cu_seqlens.shape[0]) - 1 if packed else int(k.shape[0])
-    p.n_tokens = int(k.shape[lead - 1])
+    p.dtype = dtype
+    p.batch = int(cu_seqlens.shape[0]) - 1 if packed else int(shape[0])
+    p.n_tokens = int(shape[-2])
     p.max_seqlen = int(max_seqlen) if packed else 0
-    p.n_kv_heads = int(k.shape[lead])
-    p.k_strides[:] = (0, *k.stride()[:2]) if packed else k.stride()[:3]
-    p.v_strides[:] = (0, *v.stride()[:2]) if packed else v.stride()[:3]
+    p.n_kv_heads = int(shape[-1])
+    p.k_strides[:] = (0, *k_strides) if packed else k_strides
+    p.v_strides[:] = (0, *v_strides) if packed else v_strides
     pk, p.cache_strides[:], p.max_kv_len = _kv4_cache(fn, cache, block_table, max_kv_len, p.batch)
     _kv4_tensor(fn, "pos", pos, torch.int32, cache.device, (p.batch,))
     _kv4_tensor(fn, "dev_status", dev_status, torch.int32, cache.device)
@@ -757,18 +764,26 @@ def _kv4_rows_plan(scalars, k, v, cache, pos, cu_seqlens, block_table, dev_statu
 
 
 def _kv4_read_plan(scalars, cache, pos, cu_seqlens, block_table, dev_status):
-    """The same of a read into new rows, and the shape, strides and type of these."""
+    """The same of a read into new dense rows, and the shape and type of these."""
     import torch
     fn = "diffattn_kv4_read"
     n_tokens, dtype, max_seqlen, max_kv_len = scalars
     if n_tokens is None or cache.dim() != 4:
         _kv4_fail(fn, "needs n_tokens or k and v, and a cache [., ., H, 144]")
-    rows = (n_tokens,)
+    if n_tokens < 0:
+        _kv4_fail(fn, f"n_tokens is {n_tokens}")
+    dtype = dtype or torch.bfloat16
+    codes = {torch.float32: DIFFATTN_F32, torch.bfloat16: DIFFATTN_BF16}
+    if dtype not in codes:
+        _kv4_fail(fn, f"rows are bf16 or float32, not {dtype}", -2)
+    H = cache.shape[2]
+    shape, strides = (n_tokens, H), (H * 128, 128)
     if cu_seqlens is None:
-        rows = (cache.shape[0] if block_table is None else block_table.shape[0], n_tokens)
-    k = cache.new_empty((*rows, cache.shape[2], 128), dtype=dtype or torch.bfloat16)
-    plan = _kv4_rows_plan((fn, max_seqlen, max_kv_len), k, k, cache, pos, cu_seqlens, block_table, dev_status)
-    return *plan, k.shape, k.stride(), k.dtype
+        shape = (cache.shape[0] if block_table is None else block_table.shape[0], *shape)
+        strides = (n_tokens * H * 128, *strides)
+    plan = _kv4_rows_params(fn, codes[dtype], shape, strides, strides, max_seqlen, max_kv_len, cache, pos, cu_seqlens,
+                            block_table, dev_status)
+    return *plan, (*shape, 128), dtype
 
 
 def diffattn_kv4_write(k, v, cache, pos=None, cu_seqlens=None, max_seqlen=None, block_table=None,
@@ -809,10 +824,10 @@ def diffattn_kv4_read(cache, n_tokens=None, pos=None, cu_seqlens=None, max_seqle
     raw, scope = _kv4_scope(device, stream)
     try:
         if k is None:
-            p, pk, _, shape, strides, dtype = _kv4_plan(_kv4_read_plan, (_int(n_tokens), dtype, _int(max_seqlen),
-                                                                         _int(max_kv_len)), cache, pos, cu_seqlens,
-                                                        block_table, dev_status)
-            k = torch.empty_strided(shape, strides, dtype=dtype, device=device)
+            p, pk, _, shape, dtype = _kv4_plan(_kv4_read_plan, (_int(n_tokens), dtype, _int(max_seqlen),
+                                                                _int(max_kv_len)), cache, pos, cu_seqlens,
+                                               block_table, dev_status)
+            k = torch.empty(shape, dtype=dtype, device=device)
             v = torch.empty_like(k)
         else:
             if (n_tokens is not None and int(n_tokens) != k.shape[0 if cu_seqlens is not None else 1]) or (
