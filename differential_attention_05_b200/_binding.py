@@ -638,7 +638,7 @@ def _kv4_cache(fn, cache, block_table, max_kv_len, batch):
         if cache.shape[0] != batch:
             _kv4_fail(fn, f"cache holds {cache.shape[0]} entries, the batch {batch}")
         room = int(cache.shape[1])
-        L = room if max_kv_len is None else int(max_kv_len)
+        L = room if max_kv_len is None else _int(max_kv_len)
         if L > room:
             _kv4_fail(fn, f"max_kv_len {L} is past the cache's {room} positions")
         return None, cache.stride()[:3], L
@@ -649,7 +649,7 @@ def _kv4_cache(fn, cache, block_table, max_kv_len, batch):
     pk.num_pages, pk.page_size = int(cache.shape[0]), int(cache.shape[1])
     pk.max_pages_per_seq = int(block_table.shape[1])
     pk.page_strides[:] = cache.stride()[:3]
-    L = pk.page_size * pk.max_pages_per_seq if max_kv_len is None else int(max_kv_len)
+    L = _int(pk.page_size * pk.max_pages_per_seq if max_kv_len is None else max_kv_len)
     return pk, (0, 0, 0), L
 
 
@@ -712,7 +712,13 @@ def _kv4_scope(device, stream):
 
 
 def _int(x):
-    return None if x is None else int(x)
+    """A count as the library's int32 (ctypes would drop the bits above)."""
+    if x is None:
+        return None
+    x = int(x)
+    if not -(1 << 31) <= x < 1 << 31:
+        _kv4_fail("4-bit cache", f"{x} is not an int32")
+    return x
 
 
 def _addr(t):
@@ -751,10 +757,10 @@ def _kv4_rows_params(fn, dtype, shape, k_strides, v_strides, max_seqlen, max_kv_
             _kv4_fail(fn, "cu_seqlens needs max_seqlen, the most rows of an entry")
     p = Kv4Rows()
     p.dtype = dtype
-    p.batch = int(cu_seqlens.shape[0]) - 1 if packed else int(shape[0])
-    p.n_tokens = int(shape[-2])
-    p.max_seqlen = int(max_seqlen) if packed else 0
-    p.n_kv_heads = int(shape[-1])
+    p.batch = _int(cu_seqlens.shape[0] - 1 if packed else shape[0])
+    p.n_tokens = _int(shape[-2])
+    p.max_seqlen = max_seqlen if packed else 0
+    p.n_kv_heads = _int(shape[-1])
     p.k_strides[:] = (0, *k_strides) if packed else k_strides
     p.v_strides[:] = (0, *v_strides) if packed else v_strides
     pk, p.cache_strides[:], p.max_kv_len = _kv4_cache(fn, cache, block_table, max_kv_len, p.batch)
@@ -857,7 +863,7 @@ def decode_kv4_params(q, cache, out, num_splits=0, block_table=None, max_kv_len=
     p.variant = DIFFATTN_V1 if v1 else DIFFATTN_V2
     p.dtype = _dtype_code(q)
     p.batch, p.n_q_heads, p.head_dim = int(q.shape[0]), int(q.shape[1]), int(q.shape[-1])
-    p.num_splits = int(num_splits)
+    p.num_splits = _int(num_splits)
     pk, p.kv_strides[:], p.max_kv_len = _kv4_cache(fn, cache, block_table, max_kv_len, p.batch)
     p.n_kv_heads = int(cache.shape[2])
     p.q_strides[:] = q.stride()[:2]
@@ -905,7 +911,7 @@ def diffattn_fwd_decode_kv4(q, cache, lam, kv_len=None, lambda_init=None, out=No
     out [B,Hq/2,128]. V1: q [B,H,2,64] -> out [B,H,128] (norm and scale when apply_norm, default
     on). max_kv_len defaults to the positions the cache or the block table has room for."""
     lib = load_library()
-    p, pk, need, shape, v1, _ = _kv4_plan(_kv4_decode_plan, (int(num_splits), _int(max_kv_len)), q, cache, lam, kv_len,
+    p, pk, need, shape, v1, _ = _kv4_plan(_kv4_decode_plan, (_int(num_splits), _int(max_kv_len)), q, cache, lam, kv_len,
                                           lambda_init, out, block_table, dev_status)
     device = cache.device
     raw, scope = _kv4_scope(device, stream)

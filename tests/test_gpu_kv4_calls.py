@@ -27,3 +27,24 @@ def test_a_read_allocates_its_rows_and_nothing_else(packed, dtype):
         assert k.shape == v.shape == ((617, 3, 128) if packed else (2, 617, 3, 128))
         assert k.is_contiguous() and v.is_contiguous() and k.dtype == v.dtype == (dtype or torch.bfloat16)
         assert not k.any() and not v.any()
+
+
+def test_counts_that_are_no_int32_are_refused():
+    """None is cut to its low 32 bits: max_kv_len = 2^32 + 5 once meant 5 tokens."""
+    big = (1 << 32) + 5
+    pool = torch.zeros((4, 16, 2, 144), dtype=torch.uint8, device="cuda")
+    table = torch.zeros((1, 3), dtype=torch.int32, device="cuda")
+    q = torch.zeros((1, 4, 128), dtype=torch.bfloat16, device="cuda")
+    lam = torch.zeros(2, device="cuda")
+    k = torch.zeros((1, 7, 2, 128), dtype=torch.bfloat16, device="cuda")
+    cu = torch.tensor([0, 7], dtype=torch.int32, device="cuda")
+    for call in (
+            lambda: da.diffattn_fwd_decode_kv4(q, pool, lam, block_table=table, max_kv_len=big),
+            lambda: da.diffattn_fwd_decode_kv4(q, pool, lam, block_table=table, num_splits=big),
+            lambda: da.diffattn_kv4_write(k, k, pool, block_table=table, max_kv_len=big),
+            lambda: da.diffattn_kv4_write(k[0], k[0], pool, cu_seqlens=cu, max_seqlen=big, block_table=table),
+            lambda: da.diffattn_kv4_write(k[:, :1].expand(1, big, 2, 128), k[:, :1].expand(1, big, 2, 128), pool,
+                                          block_table=table),
+            lambda: da.diffattn_kv4_read(pool, n_tokens=big, block_table=table)):
+        with pytest.raises(da.DiffattnError):
+            call()
