@@ -638,10 +638,10 @@ def _kv4_cache(fn, cache, block_table, max_kv_len, batch):
         if cache.shape[0] != batch:
             _kv4_fail(fn, f"cache holds {cache.shape[0]} entries, the batch {batch}")
         room = int(cache.shape[1])
-        L = room if max_kv_len is None else _int(max_kv_len)
+        L = room if max_kv_len is None else int(max_kv_len)
         if L > room:
             _kv4_fail(fn, f"max_kv_len {L} is past the cache's {room} positions")
-        return None, cache.stride()[:3], L
+        return None, cache.stride()[:3], _int32(fn, L)
     if block_table.dim() != 2 or block_table.shape[0] != batch:
         _kv4_fail(fn, f"block_table has shape {tuple(block_table.shape)}, the batch is {batch}")
     _kv4_tensor(fn, "block_table", block_table, torch.int32, cache.device)
@@ -649,7 +649,7 @@ def _kv4_cache(fn, cache, block_table, max_kv_len, batch):
     pk.num_pages, pk.page_size = int(cache.shape[0]), int(cache.shape[1])
     pk.max_pages_per_seq = int(block_table.shape[1])
     pk.page_strides[:] = cache.stride()[:3]
-    L = _int(pk.page_size * pk.max_pages_per_seq if max_kv_len is None else max_kv_len)
+    L = _int32(fn, pk.page_size * pk.max_pages_per_seq if max_kv_len is None else int(max_kv_len))
     return pk, (0, 0, 0), L
 
 
@@ -712,12 +712,13 @@ def _kv4_scope(device, stream):
 
 
 def _int(x):
-    """A count as the library's int32 (ctypes would drop the bits above)."""
-    if x is None:
-        return None
-    x = int(x)
+    return None if x is None else int(x)
+
+
+def _int32(fn, x):
+    """A count that a parameter struct can hold (ctypes would drop the bits above)."""
     if not -(1 << 31) <= x < 1 << 31:
-        _kv4_fail("4-bit cache", f"{x} is not an int32")
+        _kv4_fail(fn, f"{x} is not an int32")
     return x
 
 
@@ -757,10 +758,10 @@ def _kv4_rows_params(fn, dtype, shape, k_strides, v_strides, max_seqlen, max_kv_
             _kv4_fail(fn, "cu_seqlens needs max_seqlen, the most rows of an entry")
     p = Kv4Rows()
     p.dtype = dtype
-    p.batch = _int(cu_seqlens.shape[0] - 1 if packed else shape[0])
-    p.n_tokens = _int(shape[-2])
-    p.max_seqlen = max_seqlen if packed else 0
-    p.n_kv_heads = _int(shape[-1])
+    p.batch = _int32(fn, cu_seqlens.shape[0] - 1 if packed else shape[0])
+    p.n_tokens = _int32(fn, shape[-2])
+    p.max_seqlen = _int32(fn, max_seqlen) if packed else 0
+    p.n_kv_heads = _int32(fn, shape[-1])
     p.k_strides[:] = (0, *k_strides) if packed else k_strides
     p.v_strides[:] = (0, *v_strides) if packed else v_strides
     pk, p.cache_strides[:], p.max_kv_len = _kv4_cache(fn, cache, block_table, max_kv_len, p.batch)
@@ -770,7 +771,7 @@ def _kv4_rows_params(fn, dtype, shape, k_strides, v_strides, max_seqlen, max_kv_
 
 
 def _kv4_read_plan(scalars, cache, pos, cu_seqlens, block_table, dev_status):
-    """The same of a read into new dense rows, and the shape and type of these."""
+    """The same of a read into new dense rows, and the shape, strides and type of these."""
     import torch
     fn = "diffattn_kv4_read"
     n_tokens, dtype, max_seqlen, max_kv_len = scalars
@@ -789,7 +790,7 @@ def _kv4_read_plan(scalars, cache, pos, cu_seqlens, block_table, dev_status):
         strides = (n_tokens * H * 128, *strides)
     plan = _kv4_rows_params(fn, codes[dtype], shape, strides, strides, max_seqlen, max_kv_len, cache, pos, cu_seqlens,
                             block_table, dev_status)
-    return *plan, (*shape, 128), dtype
+    return *plan, torch.Size((*shape, 128)), (*strides, 1), dtype
 
 
 def diffattn_kv4_write(k, v, cache, pos=None, cu_seqlens=None, max_seqlen=None, block_table=None,
@@ -830,10 +831,10 @@ def diffattn_kv4_read(cache, n_tokens=None, pos=None, cu_seqlens=None, max_seqle
     raw, scope = _kv4_scope(device, stream)
     try:
         if k is None:
-            p, pk, _, shape, dtype = _kv4_plan(_kv4_read_plan, (_int(n_tokens), dtype, _int(max_seqlen),
-                                                                _int(max_kv_len)), cache, pos, cu_seqlens,
-                                               block_table, dev_status)
-            k = torch.empty(shape, dtype=dtype, device=device)
+            p, pk, _, shape, strides, dtype = _kv4_plan(_kv4_read_plan, (_int(n_tokens), dtype, _int(max_seqlen),
+                                                                         _int(max_kv_len)), cache, pos, cu_seqlens,
+                                                        block_table, dev_status)
+            k = torch.empty_strided(shape, strides, dtype=dtype, device=device)
             v = torch.empty_like(k)
         else:
             if (n_tokens is not None and int(n_tokens) != k.shape[0 if cu_seqlens is not None else 1]) or (
@@ -863,7 +864,7 @@ def decode_kv4_params(q, cache, out, num_splits=0, block_table=None, max_kv_len=
     p.variant = DIFFATTN_V1 if v1 else DIFFATTN_V2
     p.dtype = _dtype_code(q)
     p.batch, p.n_q_heads, p.head_dim = int(q.shape[0]), int(q.shape[1]), int(q.shape[-1])
-    p.num_splits = _int(num_splits)
+    p.num_splits = _int32(fn, int(num_splits))
     pk, p.kv_strides[:], p.max_kv_len = _kv4_cache(fn, cache, block_table, max_kv_len, p.batch)
     p.n_kv_heads = int(cache.shape[2])
     p.q_strides[:] = q.stride()[:2]
@@ -911,7 +912,7 @@ def diffattn_fwd_decode_kv4(q, cache, lam, kv_len=None, lambda_init=None, out=No
     out [B,Hq/2,128]. V1: q [B,H,2,64] -> out [B,H,128] (norm and scale when apply_norm, default
     on). max_kv_len defaults to the positions the cache or the block table has room for."""
     lib = load_library()
-    p, pk, need, shape, v1, _ = _kv4_plan(_kv4_decode_plan, (_int(num_splits), _int(max_kv_len)), q, cache, lam, kv_len,
+    p, pk, need, shape, v1, _ = _kv4_plan(_kv4_decode_plan, (int(num_splits), _int(max_kv_len)), q, cache, lam, kv_len,
                                           lambda_init, out, block_table, dev_status)
     device = cache.device
     raw, scope = _kv4_scope(device, stream)

@@ -22,3 +22,13 @@ def test_kv4_under_the_bounds_checked_library():
     tail = (r.stdout + r.stderr)[-3000:]
     assert r.returncode == 0, tail
     assert "0 out-of-range accesses skipped" in r.stdout, tail
+
+
+def test_kv4_accuracy_and_calls_under_the_bounds_checked_library():
+    env = dict(os.environ, DIFFATTN_LIBRARY=B.LIB_DEBUG, DIFFATTN_EXPECT_NO_VIOLATIONS="1")
+    cmd = [sys.executable, "-m", "pytest", "-q", "-x", "-m", "gpu", "-p", "no:cacheprovider",
+           *(os.path.join(HERE, f"test_gpu_kv4_{name}.py") for name in ("branches", "scales", "calls"))]
+    r = subprocess.run(cmd, env=env, capture_output=True, text=True, timeout=1200)
+    tail = (r.stdout + r.stderr)[-3000:]
+    assert r.returncode == 0, tail
+    assert "0 out-of-range accesses skipped" in r.stdout, tail

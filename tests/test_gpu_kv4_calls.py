@@ -48,3 +48,58 @@ def test_counts_that_are_no_int32_are_refused():
             lambda: da.diffattn_kv4_read(pool, n_tokens=big, block_table=table)):
         with pytest.raises(da.DiffattnError):
             call()
+
+
+def test_captured_behind_work_of_another_stream():
+    """A write whose rows another stream makes, captured with that stream's work, a copy and the
+    calls that read the cache: every replay follows the inputs."""
+    B, H, L = 2, 4, 500
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    src = torch.randn((2, B, 64, H, 128), generator=gen, device="cuda").bfloat16()
+    rows = torch.zeros_like(src)
+    cache = torch.zeros((B, L, H, 144), dtype=torch.uint8, device="cuda")
+    q = torch.randn((B, 8 * H, 128), generator=gen, device="cuda").bfloat16()
+    lam = torch.full((4 * H,), 0.7, device="cuda")
+    at, length = torch.zeros((2, B), dtype=torch.int32, device="cuda")
+    length += 64
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def step():
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            rows[0].copy_(src[0] * 2)
+        rows[1].copy_(src[1])
+        main.wait_stream(side)
+        da.diffattn_kv4_write(rows[0], rows[1], cache, pos=at)
+        out = da.diffattn_fwd_decode_kv4(q, cache, lam, kv_len=length)
+        long = da.diffattn_fwd_decode_kv4(q, cache, lam, kv_len=length, num_splits=3)
+        k, v = da.diffattn_kv4_read(cache, n_tokens=64, pos=at)
+        at.add_(1)
+        length.add_(1)
+        return out, long, k, v
+
+    torch.cuda.synchronize()
+    with torch.cuda.stream(main):
+        want = [[t.clone() for t in step()]]
+        for _ in range(3):
+            src.neg_()
+            want.append([t.clone() for t in step()])
+    main.synchronize()
+    src.neg_()  # four sign changes in all
+    at.zero_()
+    length.fill_(64)
+    cache.zero_()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        outs = step()
+    at.zero_()
+    length.fill_(64)
+    cache.zero_()
+    torch.cuda.synchronize()
+    for i in range(4):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want[i])), i
+        src.neg_()
+        torch.cuda.synchronize()
