@@ -21,7 +21,7 @@
 //     in as a product of the scales and -8 * 2^-24 sum q (in three bf16 parts), one MMA for 16
 //     keys, from which the scores start: half the range is all that cancels.
 //   * V nibbles become n - 8 exactly (0x6400 | n is 1024 + n). Left as subnormals with the -8
-//     from a second MMA over constants the full step took 455 us instead of 469, but the
+//     from a second MMA over constants the full step took 3% less, but the
 //     cancelling sums lost up to 2^-16 of a scale, which shows where a peaked row's key has
 //     the code 0.
 //   * Scales stay outside the MMAs: a group is two k-steps, its fp32 sums are scaled and
@@ -46,17 +46,17 @@
 //     2^-11 (p_1 - c p_2) / l_1 + 2^-11 |c / l_1 - lambda / l_2| p_2 <= 2^-11 (p_1 / l_1 +
 //     |lambda| p_2 / l_2) times its |v|, as with c = 0. (Held by the sums alone, at every
 //     fourth chunk, it let a branch 2 that rises behind a sink of both put errors of c p_2 into
-//     D that are many times O_1's own: 0.01 to 0.14 of the output.) Both branches of a unit are
-//     neighbouring columns of one lane, so this costs a dozen
-//     instructions a chunk (467 us for 447 on the full step).
+//     D that are many times O_1's own: 0.009 to 0.09 of the output.) Both branches of a unit are
+//     neighbouring columns of one lane, so this costs a dozen instructions a chunk (467 us for
+//     447 on the full step).
 //   * q is taken times a power of two per row so that its largest element is in [2^14, 2^15);
 //     fp16 then holds elements above 2^-31 of the largest exactly in even channels, and above
 //     2^-27 in odd ones, which are divided by 16.
 //
 // What bounds it: power, then issue slots. V2, 64 entries x 32768 tokens x 8 heads (2.42 GB, 374
-// us at the copy rate): 467 us alone, 510 to 550 us call after call, when the GPU holds its 1000
-// W at 1665 MHz. 32 keys of a head are about 540 warp instructions, 224 of them unpacking; with
-// the data in L2 the same loop takes no less. V1, 32 x 32768 x 16: 461 us.
+// us at the copy rate): 469 us alone, 510 to 550 us call after call, when the GPU holds its 1000
+// W at 1690 MHz. 32 keys of a head are about 540 warp instructions, 224 of them unpacking; with
+// the data in L2 the same loop took no less. V1, 32 x 32768 x 16: 463 us alone, 522 at 1730 MHz.
 #include <cuda_fp16.h>
 
 #include <string.h>

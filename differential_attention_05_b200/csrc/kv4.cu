@@ -15,9 +15,10 @@
 // meet, having two 8-bit significands). A second such constant then rounds to an integer.
 //
 // Both kernels move bytes, and what bounds the write of bf16 rows is still issue slots: 97
-// instructions a record (65536 tokens x 8 heads, 61 us where the bytes need 53; 107 us with a
-// warp to a record and 164 instructions, 76 us with 125). Reading them takes 55 us, fp32 rows of
-// 16384 tokens 25 us either way for 24 of bytes. A half-warp takes a record: lanes 0..7 its K
+// instructions a record (65536 tokens x 8 heads, 60 us where the bytes need 53; 107 us with a
+// warp to a record and 164 instructions, 76 us with 125; 74 us for as many records of 1, 2, 3 or 6
+// heads, which share rows less and spill). Reading them takes 55 us, fp32 rows of
+// 16384 tokens 26 us either way for 24 of bytes. A half-warp takes a record: lanes 0..7 its K
 // row, 8..15 its V row, each lane channels 8 c .. 8 c + 7 and 64 more of them further on, so the
 // rows are runs of 128 bytes and four lanes share a scale. A warp takes 2 STEPS records,
 // neighbouring heads first and then the next tokens, with the loads of all in flight together.

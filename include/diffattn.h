@@ -520,6 +520,7 @@ int diffattn_kv4_write(const diffattn_kv4_rows* p, const diffattn_paged_kv* pk, 
  * Arguments as for diffattn_kv4_write, with k and v written. A row whose position lies outside
  * [0, max_kv_len), or whose page lies outside the pool, reads as zeros and is reported through
  * dev_status; rows of a skipped entry, and rows of k and v that no entry owns, are not written.
+ * No two rows of k and v may overlap.
  */
 int diffattn_kv4_read(const diffattn_kv4_rows* p, const diffattn_paged_kv* pk, const void* cache,
                       const int32_t* block_table, const int32_t* cu_seqlens, const int32_t* pos,
