@@ -41,12 +41,13 @@
 //     the operand of branch 1 is p_1 - c p_2, formed in fp32: D = O_1 - c O_2 carries errors of
 //     its own size only, those of O_2 cancel as far as c is near lambda l_1 / l_2, and
 //     O_1 = D + c O_2 is put together in fp32 when the warp is done. c is that ratio of the
-//     sums so far (0 to 1), but no larger than lets 0 <= c p_2 <= p_1 for every key that meets
+//     sums so far (0 to 1), but no larger than keeps c p_2 <= 1.25 p_1 for every key that meets
 //     it. That is what makes it safe: a key's rounding errors then move the output by at most
-//     2^-11 (p_1 - c p_2) / l_1 + 2^-11 |c / l_1 - lambda / l_2| p_2 <= 2^-11 (p_1 / l_1 +
-//     |lambda| p_2 / l_2) times its |v|, as with c = 0. (Held by the sums alone, at every
-//     fourth chunk, it let a branch 2 that rises behind a sink of both put errors of c p_2 into
-//     D that are many times O_1's own: 0.009 to 0.09 of the output.) Both branches of a unit are
+//     2^-11 (|p_1 - c p_2| / l_1 + |c / l_1 - lambda / l_2| p_2) <= 2^-11 (1.5 p_1 / l_1 +
+//     |lambda| p_2 / l_2) times its |v|, where c = 0 has 1 for the 1.5. (The room of 1.25 leaves
+//     c alone under flat scores: with 1, V1's error at lambda = 1 was 0.0021, not 0.0017. Held by the sums alone, at every
+//     fourth chunk, c let a branch 2 that rises behind a sink of both put errors of c p_2 into D
+//     that are many times O_1's own: 0.009 to 0.09 of the output.) Both branches of a unit are
 //     neighbouring columns of one lane, so this costs a dozen instructions a chunk (467 us for
 //     447 on the full step).
 //   * q is taken times a power of two per row so that its largest element is in [2^14, 2^15);
@@ -70,8 +71,9 @@ namespace {
 constexpr int W = kKv4Width;
 constexpr int KEYS = 32;      // keys that a warp takes of a chunk
 constexpr int kTop = 9;       // p * scale < 2^kTop in units of 2^E when the maximum is raised ...
-constexpr float kSlack = 6.f; // ... and < 2^(kTop + kSlack) before, inside fp16's range: p_1 - c p_2 <= p_1
+constexpr float kSlack = 6.f; // ... and < 2^(kTop + kSlack) before, inside fp16's range: |p_1 - c p_2| <= p_1
 constexpr int kLeastE = -102; // the exponent E of the V scales: scales that are held are 2^-103 and more
+constexpr float kRoom = 0.32192809f;  // log2(1.25): c p_2 <= 1.25 p_1
 constexpr float kJoin = 1.f / (1 << 30) / 64.f;  // see the join's weights
 
 // A block has CW warps that compute and one that issues the copies; three blocks to an SM.
@@ -525,8 +527,8 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm)
     const bool is_unit = row0 + 2 * tq < a.group;  // columns 2 tq, 2 tq + 1: the branches of unit u
     const int u = a.v1 ? g : (g * a.group + row0 + 2 * tq) >> 1;
     const float lam = is_unit ? __ldg(a.lambda + u) : 0.f;
-    float c = 0.f;  // column 2 tq accumulates p_1 - c p_2; c >= 0, and c p_2 <= p_1 for every key
-    float c_room = INFINITY;  // that holds for keys with log2 (p_2 / p_1) up to here
+    float c = 0.f;            // column 2 tq accumulates p_1 - c p_2, c >= 0
+    float c_room = INFINITY;  // kRoom - log2(c): c p_2 <= 1.25 p_1 for keys with log2(p_2 / p_1) up to here
     // [group][tile]: channels 32 g + 4 gq + 2 tile + {0, 1}; elements 0, 2 column 2 tq, 1, 3 the next
     float o[4][2][4];
 #pragma unroll
@@ -650,7 +652,7 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm)
           const float next = both ? fminf(__fmul_rn(c, __fdiv_rn(alpha[0], alpha[1])), 1.f) : 0.f;
           const float back = (__fmul_rn(alpha[0], c) - __fmul_rn(next, alpha[1])) * shrink;
           c = next;
-          c_room = -__log2f(c);
+          c_room = kRoom - __log2f(c);
           alpha[0] *= shrink;
           alpha[1] *= shrink;
 #pragma unroll
@@ -679,8 +681,8 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm)
           apart = fmaxf(apart, fmaxf(y[1].x - y[0].x, y[1].y - y[0].y));
         }
         // c is lambda l_1 / l_2 by the sums at chunks 1, 4, 16, ..., and made smaller before the
-        // operand is formed wherever a key's c p_2 would pass its p_1, with a quarter to spare so
-        // that the next such key is rare (scattered scores: some 20 times in 295 chunks; 68
+        // operand is formed wherever a key's c p_2 would pass 1.25 p_1, with a quarter of the
+        // distance to spare so that the next such key is rare (scattered scores: some 20 times in 295 chunks; 68
         // without that and with a look at the sums at 1, 2, 4, 8, ...)
         const bool by_sums = chunk == look;
         if (by_sums || __any_sync(0xffffffffu, apart > c_room)) {
@@ -696,11 +698,11 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm)
               s2 += __shfl_xor_sync(0xffffffffu, s2, s);
             }
             next = s2 > 0.f ? fminf(fmaxf(__fmul_rn(lam, __fdiv_rn(s1, s2)), 0.f), 1.f) : 0.f;
-            c_room = -__log2f(next);
+            c_room = kRoom - __log2f(next);
           }
           if (apart > c_room) {
-            c_room = 1.25f * apart;
-            next = ex2(-c_room);
+            next = ex2(-1.25f * apart);
+            c_room = fmaf(1.25f, apart, kRoom);
           }
           const float back = c - next;
           c = next;

@@ -549,8 +549,8 @@ int diffattn_kv4_read(const diffattn_kv4_rows* p, const diffattn_paged_kv* pk, c
  * elements under 2^-27 of a row's largest lose bits, and rows with elements past 2^117
  * overflow), scales, sums and softmax statistics in fp32, probability times V scale (branch 1:
  * p_1 - c p_2 with c near lambda l_1 / l_2, as in the prefill, but no larger than keeps c p_2
- * <= p_1 for every key, so that no key's rounding counts for more than with c = 0) rounded once
- * to fp16 (2^-11; products under 2^-22 of the row's largest probability times the largest V
+ * <= 1.25 p_1 for every key, so that no key's rounding counts for more than 1.5 times what it
+ * does with c = 0) rounded once to fp16 (2^-11; products under 2^-22 of the row's largest probability times the largest V
  * scale lose bits). The softmax's sums follow the scores alone, whatever the sizes of V. No
  * atomics: results do not depend on scheduling.
  * A block-table entry outside the pool is handled as by diffattn_fwd_decode_paged. Host-side

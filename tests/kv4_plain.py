@@ -60,8 +60,9 @@ def decode(q, rec, lam, kv_len, variant, lambda_init=None, apply_norm=False, eps
     """q [B, Hq, 128] or [B, H, 2, 64], rec [B, L, H, 144] -> (out [B, units, 128], bound).
 
     The bound, element by element. A probability times a V scale is rounded to fp16 (2^-11; the
-    kernel's p_1 - c p_2 for branch 1 has 0 <= c p_2 <= p_1, so 2^-11 of it for branch 1 and
-    2^-11 |c / l_1 - lambda / l_2| p_2 for branch 2 add up to no more than with c = 0);
+    kernel's p_1 - c p_2 for branch 1 has 0 <= c p_2 <= 1.25 p_1, and 2^-11 of its size for branch
+    1 and 2^-11 |c / l_1 - lambda / l_2| p_2 for branch 2 add up to no more than with c = 0 unless
+    a key has c p_2 > p_1 and c is over 5 lambda l_1 / l_2, and then to 1.5 times that at most);
     fp32 rounding of the scores moves x by at most 40 steps of 2^-24 on the sum of magnitudes
     sum |q| |scale| 24 (nibbles to 15 and the start of 8, products added in MMAs of 16 and then
     over 4 groups), and p by that times ln 2 in relative terms, numerator and denominator

@@ -1,11 +1,13 @@
 """The decode over a 4-bit cache where its two branches attend different keys: scores set key by
 key, against plain 64-bit attention over the cache's values.
 
-The bound is kv4_plain.decode's. Branch 1's operand is p_1 - c p_2 with 0 <= c p_2 <= p_1 for
-every key, so it is at most p_1 and its fp16 rounding moves O_1 by at most 2^-11 (p_1 - c p_2)
-|v|; branch 2's moves O_1 / l_1 - lambda O_2 / l_2 by 2^-11 p_2 |v| times |c / l_1 - lambda / l_2|,
-at most 2^-11 (c p_2 / l_1 + |lambda| p_2 / l_2) |v|. Together that is 2^-11 (p_1 / l_1 + |lambda|
-p_2 / l_2) |v|, the bound's first term, whatever c is."""
+The bound is kv4_plain.decode's. Branch 1's operand is p_1 - c p_2 with 0 <= c p_2 <= 1.25 p_1 for
+every key; its fp16 rounding moves O_1 by at most 2^-11 |p_1 - c p_2| |v|, branch 2's moves
+O_1 / l_1 - lambda O_2 / l_2 by 2^-11 p_2 |v| times |c / l_1 - lambda / l_2|. Where c p_2 <= p_1, both
+make at most 2^-11 (p_1 / l_1 + |lambda| p_2 / l_2) |v|, the bound's first term, whatever c is; they
+do so too where c p_2 is between that and 1.25 p_1, unless c is over 5 lambda l_1 / l_2. The scores
+here have no key or next to none of that kind: a branch 2 that rises does so by more than the
+log2(1.25) in between."""
 import numpy as np
 import pytest
 import torch
